@@ -5,13 +5,13 @@
 
 #include <atomic>
 #include <chrono>
-#include <cstdarg>
 #include <cstdio>
 #include <cstddef>
 #include <cstring>
 #include <random>
 
 #include "../../include/ep_route_topk.h"
+#include "ep_api.h"
 #include "ep_internal.h"
 
 namespace ep {
@@ -19,37 +19,20 @@ LaunchTiming& launch_timing() {
     static thread_local LaunchTiming t;
     return t;
 }
+
+char* error_text() {
+    static thread_local char text[kErrorText] = "";
+    return text;
+}
 }  // namespace ep
 
 namespace {
 
-thread_local char g_err[512] = "";
-
-// Clears the one-shot timing hook when a compute entry point returns.
-struct TimingScope {
-    ~TimingScope() { ep::launch_timing() = ep::LaunchTiming{}; }
-};
-
-ep_status fail(ep_status st, const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof(g_err), fmt, ap);
-    va_end(ap);
-    return st;
-}
-
-ep_status ok() {
-    g_err[0] = '\0';
-    return EP_OK;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-ep_status launched(hipError_t e, const char* what) {
-    if (e != hipSuccess)
-        return fail(EP_ERR_LAUNCH, "%s: launch failed: %s", what, hipGetErrorString(e));
-    return ok();
-}
+using ep::aligned;
+using ep::fail;
+using ep::launched;
+using ep::ok;
+using ep::TimingScope;
 
 // Sizes shared by route / layout / fused.
 ep_status check_routing_sizes(const char* fn, int32_t T, int32_t k, int32_t E) {
@@ -76,20 +59,6 @@ ep_status check_rows(const char* fn, int32_t T, int32_t H, int32_t k) {
     return EP_OK;
 }
 
-#define EP_REQUIRE_PTR(fn, p, a)                                                     \
-    do {                                                                             \
-        if (!(p)) return fail(EP_ERR_INVALID_ARG, "%s: %s is NULL", fn, #p);         \
-        if (!aligned((p), (a)))                                                      \
-            return fail(EP_ERR_INVALID_ARG, "%s: %s is not %d-byte aligned", fn, #p, \
-                        int(a));                                                     \
-    } while (0)
-
-#define EP_TRY(expr)                  \
-    do {                              \
-        ep_status st_ = (expr);       \
-        if (st_ != EP_OK) return st_; \
-    } while (0)
-
 }  // namespace
 
 extern "C" {
@@ -109,7 +78,7 @@ const char* ep_status_string(ep_status status) {
     }
 }
 
-const char* ep_last_error(void) { return g_err; }
+const char* ep_last_error(void) { return ep::error_text(); }
 
 ep_status ep_set_timing_events(void* start_event, void* stop_event)
 {

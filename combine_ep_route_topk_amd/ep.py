@@ -68,6 +68,17 @@ _SIGS = {
                           _P, ctypes.c_int64, _P, _P], ctypes.c_int),
     "ep_window_copy": ([_P, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _i32, _P, _P, _P],
                        ctypes.c_int),
+    "ep_quantize_fp8": ([_P, _i32, _i32, _P, _P, _P], ctypes.c_int),
+    "ep_dispatch_fp8": ([_P, _i32, _i32, _i32, _P, _P, _P, _P], ctypes.c_int),
+    "ep_quantize_weight_fp8": ([_P, _i32, _i32, _i32, _P, _P, _P, _P, _P], ctypes.c_int),
+    "ep_expert_gemm_fp8": ([_P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P], ctypes.c_int),
+    "ep_expert_swiglu_fp8": ([_P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P, _P, _P],
+                             ctypes.c_int),
+    "ep_swiglu_grad": ([_P, _P, _i32, _i32, _P, _P, _P], ctypes.c_int),
+    "ep_expert_wgrad": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P], ctypes.c_int),
+    "ep_moe_tokens_workspace_bytes": ([_i32, _i32, _i32], _sz),
+    "ep_moe_tokens": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P, _P, _P, _P, _P, _sz, _P],
+                      ctypes.c_int),
     "ep_get_device_error": ([_P, _P], ctypes.c_int),
     "ep_set_timing_events": ([_P, _P], ctypes.c_int),
 }
@@ -517,6 +528,252 @@ def ep_window_copy(src: torch.Tensor, dst: torch.Tensor, row_bytes: int, S: int,
     _check(_lib.ep_window_copy(_ptr(src), _ptr(dst), row_bytes, S, _ptr(tasks), _ptr(core_begin),
                                _ptr(slice_start), C, _ptr(core_clock), _ptr(bad),
                                _P(_stream(stream, src.device))))
+
+
+# ------------------------------------------------------------------- experts
+SCALE_BLOCK = 128        # values that share one power-of-two scale (a byte b: 2^(b - 127))
+MOE_MAX_TOKENS = 64      # largest batch of ep_moe_tokens
+
+
+def scale_blocks(n: int) -> int:
+    return -(-n // SCALE_BLOCK)
+
+
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+_SCALE = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _need_one_of(t: torch.Tensor, name: str, dtypes: tuple, shape: tuple | None = None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
+    _need(t, name, t.dtype, shape)
+
+
+def _shape(t: torch.Tensor, name: str, dims: int) -> tuple:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return tuple(t.shape)
+
+
+def _launch(fn, dev, stream, tensors, *args) -> None:
+    """Calls `fn` for tensors of one device, which is made current around the
+    call when it is not (a null stream belongs to the current device)."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors lie on different devices: {t.device} and {dev}")
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _P(_stream(stream, dev))))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _P(_stream(stream, dev))))
+
+
+def ep_quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None,
+                    scale: torch.Tensor | None = None, stream=None):
+    """x bf16 [S][H] -> (q e4m3 [S][H], scale u8 [S][ceil(H/128)])."""
+    S, H = _shape(x, "x", 2)
+    _bits_ok(x, "x")
+    dev, nb = x.device, scale_blocks(H)
+    if q is None:
+        q = torch.empty((S, H), dtype=torch.float8_e4m3fn, device=dev)
+    if scale is None:
+        scale = torch.empty((S, nb), dtype=torch.uint8, device=dev)
+    _need_one_of(q, "q", _FP8, (S, H))
+    _need_one_of(scale, "scale", _SCALE, (S, nb))
+    _launch(_lib.ep_quantize_fp8, dev, stream, (q, scale), _ptr(x), S, H, _ptr(q), _ptr(scale))
+    return q, scale
+
+
+def ep_dispatch_fp8(x: torch.Tensor, pos: torch.Tensor, send: torch.Tensor | None = None,
+                    scale: torch.Tensor | None = None, stream=None):
+    """x bf16 [T][H], pos i32 [T][k] -> (send e4m3 [T*k][H], scale u8 [T*k][ceil(H/128)])."""
+    T, H = _shape(x, "x", 2)
+    _bits_ok(x, "x")
+    k = _shape(pos, "pos", 2)[1]
+    _need(pos, "pos", torch.int32, (T, k))
+    dev, nb = x.device, scale_blocks(H)
+    if send is None:
+        send = torch.empty((T * k, H), dtype=torch.float8_e4m3fn, device=dev)
+    if scale is None:
+        scale = torch.empty((T * k, nb), dtype=torch.uint8, device=dev)
+    _need_one_of(send, "send", _FP8, (T * k, H))
+    _need_one_of(scale, "scale", _SCALE, (T * k, nb))
+    _launch(_lib.ep_dispatch_fp8, dev, stream, (pos, send, scale), _ptr(x), T, H, k, _ptr(pos),
+            _ptr(send), _ptr(scale))
+    return send, scale
+
+
+def ep_quantize_weight_fp8(w: torch.Tensor, transposed: bool = False, out: dict | None = None,
+                           stream=None) -> dict:
+    """w bf16 [E][N][K] -> dict(q e4m3 [E][N][K], scale u8 [E][ceil(N/128)][ceil(K/128)]); with
+    `transposed` also q_t [E][K][N] and scale_t, the same values."""
+    E, N, K = _shape(w, "w", 3)
+    _bits_ok(w, "w")
+    dev, nb, kb = w.device, scale_blocks(N), scale_blocks(K)
+    if out is None:
+        f8 = dict(dtype=torch.float8_e4m3fn, device=dev)
+        u8 = dict(dtype=torch.uint8, device=dev)
+        out = dict(q=torch.empty((E, N, K), **f8), scale=torch.empty((E, nb, kb), **u8))
+        if transposed:
+            out |= dict(q_t=torch.empty((E, K, N), **f8), scale_t=torch.empty((E, kb, nb), **u8))
+    _need_one_of(out["q"], "q", _FP8, (E, N, K))
+    _need_one_of(out["scale"], "scale", _SCALE, (E, nb, kb))
+    q_t = scale_t = None
+    if transposed:
+        q_t, scale_t = out["q_t"], out["scale_t"]
+        _need_one_of(q_t, "q_t", _FP8, (E, K, N))
+        _need_one_of(scale_t, "scale_t", _SCALE, (E, kb, nb))
+    _launch(_lib.ep_quantize_weight_fp8, dev, stream, (out["q"], out["scale"], q_t, scale_t),
+            _ptr(w), E, N, K, _ptr(out["q"]), _ptr(out["scale"]), _ptr(q_t), _ptr(scale_t))
+    return out
+
+
+def _expert_operands(a, a_scale, w, w_scale, expert_offsets, w_name):
+    S, K = _shape(a, "a", 2)
+    _need_one_of(a, "a", _FP8)
+    _need_one_of(a_scale, "a_scale", _SCALE, (S, scale_blocks(K)))
+    E, N, _ = _shape(w, w_name, 3)
+    _need_one_of(w, w_name, _FP8, (E, N, K))
+    _need_one_of(w_scale, w_name + "_scale", _SCALE, (E, scale_blocks(N), scale_blocks(K)))
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    return S, N, K, E
+
+
+def ep_expert_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
+                       w_scale: torch.Tensor, expert_offsets: torch.Tensor,
+                       y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """a e4m3 [S][K] with a_scale, w e4m3 [E][N][K] with w_scale, expert_offsets i32 [E+1]
+    -> y bf16 [S][N], y[s] = W[e(s)] a[s]."""
+    S, N, K, E = _expert_operands(a, a_scale, w, w_scale, expert_offsets, "w")
+    dev = a.device
+    if y is None:
+        y = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
+    _bits_ok(y, "y", (S, N))
+    _launch(_lib.ep_expert_gemm_fp8, dev, stream, (a_scale, w, w_scale, expert_offsets, y),
+            _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), S, N, K, E,
+            _ptr(y))
+    return y
+
+
+def ep_expert_swiglu_fp8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tensor,
+                         w13_scale: torch.Tensor, expert_offsets: torch.Tensor,
+                         h: torch.Tensor | None = None, h_scale: torch.Tensor | None = None,
+                         gate_up: torch.Tensor | None = None, save_gate_up: bool = False,
+                         stream=None):
+    """a e4m3 [S][K] with a_scale, w13 e4m3 [E][2I][K] (gate rows, then up rows) with w13_scale
+    -> (h e4m3 [S][I], h_scale u8 [S][I/128], gate_up bf16 [S][2I] or None): h = silu(g) * u
+    quantised.  gate_up is written when it is passed in or save_gate_up is true."""
+    S, N, K, E = _expert_operands(a, a_scale, w13, w13_scale, expert_offsets, "w13")
+    if N % 2:
+        raise ValueError("w13 must hold as many gate rows as up rows")
+    dev, I = a.device, N // 2
+    if h is None:
+        h = torch.empty((S, I), dtype=torch.float8_e4m3fn, device=dev)
+    if h_scale is None:
+        h_scale = torch.empty((S, scale_blocks(I)), dtype=torch.uint8, device=dev)
+    if gate_up is None and save_gate_up:
+        gate_up = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
+    _need_one_of(h, "h", _FP8, (S, I))
+    _need_one_of(h_scale, "h_scale", _SCALE, (S, scale_blocks(I)))
+    if gate_up is not None:
+        _bits_ok(gate_up, "gate_up", (S, N))
+    _launch(_lib.ep_expert_swiglu_fp8, dev, stream,
+            (a_scale, w13, w13_scale, expert_offsets, h, h_scale, gate_up),
+            _ptr(a), _ptr(a_scale), _ptr(w13), _ptr(w13_scale), _ptr(expert_offsets), S, I, K, E,
+            _ptr(h), _ptr(h_scale), _ptr(gate_up))
+    return h, h_scale, gate_up
+
+
+def ep_swiglu_grad(grad_h: torch.Tensor, gate_up: torch.Tensor,
+                   grad_gate_up: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                   stream=None):
+    """grad_h bf16 [S][I], gate_up bf16 [S][2I] -> (grad_gate_up bf16 [S][2I], h bf16 [S][I])."""
+    S, I = _shape(grad_h, "grad_h", 2)
+    _bits_ok(grad_h, "grad_h")
+    _bits_ok(gate_up, "gate_up", (S, 2 * I))
+    dev = grad_h.device
+    if grad_gate_up is None:
+        grad_gate_up = torch.empty((S, 2 * I), dtype=gate_up.dtype, device=dev)
+    if h is None:
+        h = torch.empty((S, I), dtype=grad_h.dtype, device=dev)
+    _bits_ok(grad_gate_up, "grad_gate_up", (S, 2 * I))
+    _bits_ok(h, "h", (S, I))
+    _launch(_lib.ep_swiglu_grad, dev, stream, (gate_up, grad_gate_up, h), _ptr(grad_h),
+            _ptr(gate_up), S, I, _ptr(grad_gate_up), _ptr(h))
+    return grad_gate_up, h
+
+
+def ep_expert_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor,
+                    grad_w: torch.Tensor | None = None, accumulate: bool = False,
+                    stream=None) -> torch.Tensor:
+    """grad_y bf16 [S][N], x bf16 [S][K], expert_offsets i32 [E+1] -> grad_w f32 [E][N][K];
+    `accumulate` adds to the grad_w passed in."""
+    S, N = _shape(grad_y, "grad_y", 2)
+    K = _shape(x, "x", 2)[1]
+    _bits_ok(grad_y, "grad_y")
+    _bits_ok(x, "x", (S, K))
+    E = _shape(expert_offsets, "expert_offsets", 1)[0] - 1
+    _need(expert_offsets, "expert_offsets", torch.int32)
+    if E < 1:
+        raise ValueError("expert_offsets must hold E + 1 >= 2 values")
+    dev = grad_y.device
+    if grad_w is None:
+        if accumulate:
+            raise ValueError("accumulate needs the grad_w to add to")
+        grad_w = torch.empty((E, N, K), dtype=torch.float32, device=dev)
+    _need(grad_w, "grad_w", torch.float32, (E, N, K))
+    _launch(_lib.ep_expert_wgrad, dev, stream, (x, expert_offsets, grad_w), _ptr(grad_y), _ptr(x),
+            _ptr(expert_offsets), S, N, K, E, int(bool(accumulate)), _ptr(grad_w))
+    return grad_w
+
+
+def ep_moe_tokens_workspace_bytes(T: int, k: int, I: int) -> int:
+    return int(_lib.ep_moe_tokens_workspace_bytes(T, k, I))
+
+
+def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                  w13: torch.Tensor, w2: torch.Tensor, w13_scale: torch.Tensor | None = None,
+                  w2_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x bf16 [T][H] (T <= 64), topk_idx i32 [T][k], topk_w f32 [T][k], w13 [E][2I][H] (gate rows,
+    then up rows), w2 [E][H][I], e4m3 with their scales or bf16 without -> out bf16 [T][H]: the
+    whole layer.  Calls that overlap need a `workspace` each (by default every call gets its own)."""
+    T, H = _shape(x, "x", 2)
+    _bits_ok(x, "x")
+    k = _shape(topk_idx, "topk_idx", 2)[1]
+    _need(topk_idx, "topk_idx", torch.int32, (T, k))
+    _need(topk_w, "topk_w", torch.float32, (T, k))
+    E, N, _ = _shape(w13, "w13", 3)
+    if N % 2:
+        raise ValueError("w13 must hold as many gate rows as up rows")
+    I = N // 2
+    if (w13_scale is None) != (w2_scale is None):
+        raise ValueError("w13_scale and w2_scale go together")
+    if w13_scale is None:
+        _bits_ok(w13, "w13", (E, N, H))
+        _bits_ok(w2, "w2", (E, H, I))
+    else:
+        _need_one_of(w13, "w13", _FP8, (E, N, H))
+        _need_one_of(w2, "w2", _FP8, (E, H, I))
+        _need_one_of(w13_scale, "w13_scale", _SCALE, (E, scale_blocks(N), scale_blocks(H)))
+        _need_one_of(w2_scale, "w2_scale", _SCALE, (E, scale_blocks(H), scale_blocks(I)))
+    dev = x.device
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+    if workspace is None:
+        workspace = torch.empty(ep_moe_tokens_workspace_bytes(T, k, I), dtype=torch.uint8,
+                                device=dev)
+    _bits_ok(out, "out", (T, H))
+    _need(workspace, "workspace", torch.uint8)
+    _launch(_lib.ep_moe_tokens, dev, stream,
+            (topk_idx, topk_w, w13, w2, w13_scale, w2_scale, out, workspace),
+            _ptr(x), _ptr(topk_idx), _ptr(topk_w), T, H, I, E, k, _ptr(w13), _ptr(w13_scale),
+            _ptr(w2), _ptr(w2_scale), _ptr(out), _ptr(workspace), workspace.numel())
+    return out
 
 
 # ------------------------------------------------------------------- bound calls

@@ -73,8 +73,8 @@ const char* ep_last_error(void);
  * device work only).  After this call, the NEXT compute entry point called on
  * the same thread (ep_route_topk, ep_dispatch_layout, ep_dispatch, ep_combine,
  * ep_combine_grad, ep_dispatch_grad, ep_fused_dispatch_combine[_sync],
- * ep_expert_slices, ep_window_copy, ep_rank_coalesce, ep_expand_records) records `start_event` when
- * its first kernel
+ * ep_expert_slices, ep_window_copy, ep_rank_coalesce, ep_expand_records, and the expert
+ * operators) records `start_event` when its first kernel
  * starts and `stop_event` when its last kernel ends, taken from the kernels'
  * own dispatch packets -- the same interval a kernel-trace profiler reports,
  * with no marker packet in between.  Either event may be NULL.  The hook then
@@ -486,6 +486,128 @@ ep_status ep_expand_records(const uint16_t* rows, const uint64_t* masks, int32_t
  * EP_ERR_INVALID_ARG otherwise or for a NULL peer with N > 1.
  * ------------------------------------------------------------------------- */
 ep_status ep_exchange_waves(int32_t N, int32_t* peer);
+
+/* ---------------------------------------------------------------------------
+ * Experts.  The operators between dispatch and combine: 8-bit rows and weights,
+ * the experts' products over the expert-contiguous buffer, their gradients, and
+ * the whole layer for a few tokens.
+ *
+ * 8-bit values are e4m3 (OCP: largest 448, no infinity).  They carry one scale
+ * for each block of 128: a row of H values has ceil(H/128) scales, a weight
+ * matrix [N][K] has [ceil(N/128)][ceil(K/128)], one for each 128 x 128 block.
+ * A scale is a power of two held as one byte b: 2^(b - 127) (E8M0; 255 is NaN).
+ * The quantisers pick the least one with max|x| / scale <= 448 over the block
+ * (bytes 1 .. 247; 1.0 for a block of zeros); a value is rounded once, to
+ * nearest even.  Infinities and NaN become NaN and leave the block's scale to
+ * its finite values.
+ *
+ * Rows belong to experts by expert_offsets i32 [E+1] (ep_dispatch_layout's, or
+ * ep_expand_records'): expert e has rows [expert_offsets[e],
+ * expert_offsets[e+1]) of S.  An expert may have no rows.  Output rows outside
+ * every segment are left as they were.  Offsets are clamped to [0, S]; ones that
+ * decrease give unspecified rows, never an access out of bounds.
+ *
+ * Sizes: 0 <= S < 2^30 (S = 0: nothing is enqueued and the row buffers may be
+ * NULL, except that ep_expert_wgrad writes its zeros), E <= 1024, N, K, I <=
+ * 2^17 and multiples of 16 (8 where no 8-bit operand is involved); a tile
+ * count past the launch limits is EP_ERR_LAUNCH.  Buffers 16-byte aligned,
+ * scales any.  No call needs a workspace but ep_moe_tokens; none keeps state,
+ * so calls on several streams and captured ones are independent.
+ *
+ * ep_quantize_fp8: rows as they are.
+ *   x bf16 [S][H]   q e4m3 [S][H] out   scale u8 [S][ceil(H/128)] out.  H % 16 == 0.
+ * ep_dispatch_fp8: ep_dispatch with the rows quantised on the way, each row
+ * once: send[pos[t][j]] and scale[pos[t][j]] hold x[t]'s.  pos entries outside
+ * [0, T*k) are skipped.  T >= 1.
+ *   send e4m3 [T*k][H] out   scale u8 [T*k][ceil(H/128)] out.
+ * ep_quantize_weight_fp8: weights, and with q_t and scale_t (both or neither)
+ * also the transposed matrices, the same values: what the input gradient
+ * multiplies by.
+ *   w bf16 [E][N][K]   q e4m3 [E][N][K] out   scale u8 [E][ceil(N/128)][ceil(K/128)] out
+ *   q_t e4m3 [E][K][N] out   scale_t u8 [E][ceil(K/128)][ceil(N/128)] out.
+ * ------------------------------------------------------------------------- */
+ep_status ep_quantize_fp8(const uint16_t* x, int32_t S, int32_t H, uint8_t* q, uint8_t* scale,
+                          void* stream);
+ep_status ep_dispatch_fp8(const uint16_t* x, int32_t T, int32_t H, int32_t k, const int32_t* pos,
+                          uint8_t* send, uint8_t* scale, void* stream);
+ep_status ep_quantize_weight_fp8(const uint16_t* w, int32_t E, int32_t N, int32_t K, uint8_t* q,
+                                 uint8_t* scale, uint8_t* q_t, uint8_t* scale_t, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Grouped product: y[s] = W[e] a[s] for every row s of every expert e, summed in
+ * f32 and rounded once to bf16 (nearest even).  With ep_quantize_weight_fp8's
+ * transposed weights and the quantised gradient of y as `a` it is the input
+ * gradient.
+ *   a e4m3 [S][K], a_scale u8 [S][ceil(K/128)]
+ *   w e4m3 [E][N][K], w_scale u8 [E][ceil(N/128)][ceil(K/128)]
+ *   y bf16 [S][N] out.
+ * ------------------------------------------------------------------------- */
+ep_status ep_expert_gemm_fp8(const uint8_t* a, const uint8_t* a_scale, const uint8_t* w,
+                             const uint8_t* w_scale, const int32_t* expert_offsets, int32_t S,
+                             int32_t N, int32_t K, int32_t E, uint16_t* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The experts' first product with the gated activation and the quantisation of
+ * its result: [g; u] = W13[e] a[s] (rows [0, I) of W13 the gate, [I, 2I) the
+ * up projection), h = silu(g) * u, all in f32, then quantised in blocks of 128:
+ * what ep_expert_gemm_fp8 takes with the second weights.
+ *   w13 e4m3 [E][2I][K], w13_scale u8 [E][2I/128][ceil(K/128)]; I % 128 == 0,
+ *   2*I*K < 2^31
+ *   h e4m3 [S][I] out, h_scale u8 [S][I/128] out
+ *   gate_up bf16 [S][2I] out, or NULL: g and u rounded, for ep_swiglu_grad.
+ * ------------------------------------------------------------------------- */
+ep_status ep_expert_swiglu_fp8(const uint8_t* a, const uint8_t* a_scale, const uint8_t* w13,
+                               const uint8_t* w13_scale, const int32_t* expert_offsets, int32_t S,
+                               int32_t I, int32_t K, int32_t E, uint8_t* h, uint8_t* h_scale,
+                               uint16_t* gate_up, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gradient of the gated activation over S rows: with sig = 1 / (1 + exp(-g)),
+ *   grad g = grad_h u (sig + g sig (1 - sig)),  grad u = grad_h g sig,
+ * in f32, each rounded once.
+ *   grad_h bf16 [S][I], gate_up bf16 [S][2I] (gate, then up)
+ *   grad_gate_up bf16 [S][2I] out
+ *   h bf16 [S][I] out, or NULL: silu(g) * u, what the second weights' gradient
+ *   needs.  I % 8 == 0.
+ * ------------------------------------------------------------------------- */
+ep_status ep_swiglu_grad(const uint16_t* grad_h, const uint16_t* gate_up, int32_t S, int32_t I,
+                         uint16_t* grad_gate_up, uint16_t* h, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Weight gradients: grad_w[e][n][k] = sum over the rows s of expert e of
+ * grad_y[s][n] * x[s][k], in f32 in an order fixed by the sizes and offsets.
+ * accumulate != 0 adds to grad_w instead of overwriting it; an expert without
+ * rows gets zeros (or is left as it was).
+ *   grad_y bf16 [S][N], x bf16 [S][K]; N % 8 == K % 8 == 0
+ *   grad_w f32 [E][N][K] out.
+ * ------------------------------------------------------------------------- */
+ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32_t* expert_offsets,
+                          int32_t S, int32_t N, int32_t K, int32_t E, int32_t accumulate,
+                          float* grad_w, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The whole layer for 1 <= T <= 64 tokens (one decoding step), in two launches:
+ *   out[t] = sum_j topk_w[t][j] W2[e] (silu(g) * u), [g; u] = W13[e] x[t],
+ *   e = topk_idx[t][j].
+ * Activations are not quantised; sums are f32 and out is rounded once.  Each
+ * picked expert's weights are read once, whatever the tokens that picked it.
+ * A pick outside [0, E) contributes nothing (a token without any gets zeros);
+ * an expert picked twice by a token counts with both weights.  The result is
+ * the same on every call.
+ *   x bf16 [T][H], topk_idx i32 [T][k], topk_w f32 [T][k]
+ *   w13 [E][2I][H] (gate rows, then up rows), w2 [E][H][I]: e4m3 with w13_scale
+ *   u8 [E][2I/128][ceil(H/128)] and w2_scale u8 [E][ceil(H/128)][I/128], or bf16
+ *   when both scales are NULL.  H % 16 == 0; I % 128 == 0 (8-bit) or I % 16 == 0.
+ *   out bf16 [T][H] out
+ *   workspace ep_moe_tokens_workspace_bytes(T, k, I) bytes, 256-byte aligned;
+ *   contents need no initialisation.  Calls that share one must not overlap.
+ * T > 64 is EP_ERR_UNSUPPORTED: dispatch and the grouped products take more.
+ * ------------------------------------------------------------------------- */
+size_t ep_moe_tokens_workspace_bytes(int32_t T, int32_t k, int32_t I);
+ep_status ep_moe_tokens(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, int32_t T,
+                        int32_t H, int32_t I, int32_t E, int32_t k, const void* w13,
+                        const uint8_t* w13_scale, const void* w2, const uint8_t* w2_scale,
+                        uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Reads a layout or fused workspace's error word: synchronises `stream` first,
