@@ -7,25 +7,12 @@
 // accumulators never leave the matrix core's registers: no multiply-add per
 // block on the vector ALU.  The weights are its row operand: a lane then holds
 // four neighbouring n of one token.
-#include "experts_internal.h"
+#include "expert_gemm_large.h"
 
 namespace ep {
 namespace {
 
 constexpr int kBK = kScaleBlock;          // bytes of k per step = one scale block
-
-struct GemmArgs {
-    const uint8_t* a;
-    const uint8_t* a_scale;
-    const uint8_t* w;
-    const uint8_t* w_scale;
-    const int32_t* offsets;
-    int S, N, K, E;      // N: rows of one expert's weights (2 I when gated)
-    int max_tiles;       // row tiles that S rows in E segments can make
-    uint16_t* y;         // plain: [S][N]; gated: gate_up [S][N] or NULL
-    uint8_t* h;          // gated: [S][N/2]
-    uint8_t* h_scale;    // gated: [S][N/256]
-};
 
 // LDS image of a tile: rows of 128 bytes in eight 16-byte chunks, chunk c of
 // row r at slot c ^ (r / 2 % 8): 16 lanes reading the same chunk of 16
@@ -57,18 +44,9 @@ __global__ __launch_bounds__(WN* WM* kWave) void expert_gemm_kernel(GemmArgs p)
     const int wn = wave % WN, wm = wave / WN;
     const int N = p.N, K = p.K, KB = scale_blocks(K);
 
-    // ---- tile of this workgroup: eight row tiles, then the next n tile
-    const int nt = GATED ? (N / 2 + kScaleBlock - 1) / kScaleBlock : (N + TN - 1) / TN;
-    const int mt = count_row_tiles(p.offsets, p.E, p.S, TM, p.max_tiles);
-    const int total = mt * nt, per = (total + 7) / 8;
-    const int id = int(blockIdx.x % 8) * per + int(blockIdx.x / 8);
-    if (int(blockIdx.x / 8) >= per || id >= total) return;
-    constexpr int kGroup = 8;
-    const int group = id / (kGroup * nt);
-    const int gsize = mt - group * kGroup < kGroup ? mt - group * kGroup : kGroup;
-    const int in = id - group * kGroup * nt;
-    const int tile_n = in / gsize;
-    const RowTile t = find_row_tile(p.offsets, p.E, p.S, TM, group * kGroup + in % gsize);
+    const GemmTile tile = GemmTiles(p, TM, GATED ? N / 256 : (N + TN - 1) / TN).at(p, TM, 0);
+    const RowTile t = tile.rows;
+    const int tile_n = tile.n;
     if (t.expert < 0) return;
     const int rows = t.end - t.row0 < TM ? t.end - t.row0 : TM;
 
@@ -250,16 +228,36 @@ __global__ __launch_bounds__(WN* WM* kWave) void expert_gemm_kernel(GemmArgs p)
     }
 }
 
-template <int TN, int TM, int WN, int WM, bool GATED>
-hipError_t launch(GemmArgs p, hipStream_t s)
+// Grid for tiles of TM rows and nt n tiles (a multiple of 8, for the XCDs), or
+// 0 when a launch cannot hold it; sets p.max_tiles.
+uint32_t gemm_grid(GemmArgs& p, int TM, int64_t nt, int threads)
 {
     const int64_t mt = p.S / TM + (p.E < p.S ? p.E : p.S);
     p.max_tiles = int(mt);
-    const int64_t nt = GATED ? scale_blocks(p.N / 2) : (p.N + TN - 1) / TN;
     const int64_t grid = (mt * nt + 7) / 8 * 8;
-    if (grid * WN * WM * kWave >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-    EP_LAUNCH((expert_gemm_kernel<TN, TM, WN, WM, GATED>), dim3(uint32_t(grid)),
-              dim3(WN * WM * kWave), 0, s, p);
+    return grid * threads < (int64_t(1) << 31) ? uint32_t(grid) : 0;
+}
+
+template <int TN, int TM, int WN, int WM, bool GATED>
+hipError_t launch(GemmArgs p, hipStream_t s)
+{
+    const uint32_t grid = gemm_grid(p, TM, GATED ? p.N / 256 : (p.N + TN - 1) / TN, WN * WM * kWave);
+    if (!grid) return hipErrorInvalidConfiguration;
+    EP_LAUNCH((expert_gemm_kernel<TN, TM, WN, WM, GATED>), dim3(grid), dim3(WN * WM * kWave), 0, s,
+              p);
+    return hipGetLastError();
+}
+
+template <bool GATED>
+hipError_t launch_large(GemmArgs p, hipStream_t s)
+{
+    // one workgroup a CU (it takes all of the LDS), each with its share of tiles
+    uint32_t grid =
+        gemm_grid(p, kLargeTile, GATED ? p.N / 256 : (p.N + kLargeTile - 1) / kLargeTile, 1);
+    if (!grid) return hipErrorInvalidConfiguration;
+    const uint32_t cus = device_cu_count() / 8 * 8;
+    grid = grid < cus || cus == 0 ? grid : cus;
+    EP_LAUNCH((expert_gemm_large_kernel<GATED>), dim3(grid), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -270,7 +268,7 @@ hipError_t launch_expert_gemm(const uint8_t* a, const uint8_t* a_scale, const ui
                               int E, uint16_t* y, hipStream_t s)
 {
     const GemmArgs p{a, a_scale, w, w_scale, offsets, S, N, K, E, 0, y, nullptr, nullptr};
-    if (S >= 64 * E) return launch<256, 256, 2, 4, false>(p, s);
+    if (S >= 64 * E) return launch_large<false>(p, s);
     return launch<128, 32, 4, 1, false>(p, s);
 }
 
@@ -280,7 +278,7 @@ hipError_t launch_expert_swiglu(const uint8_t* a, const uint8_t* a_scale, const 
                                 hipStream_t s)
 {
     const GemmArgs p{a, a_scale, w13, w13_scale, offsets, S, 2 * I, K, E, 0, gate_up, h, h_scale};
-    if (S >= 64 * E) return launch<256, 256, 2, 4, true>(p, s);
+    if (S >= 64 * E) return launch_large<true>(p, s);
     return launch<256, 32, 4, 1, true>(p, s);
 }
 

@@ -145,6 +145,8 @@ SHAPES = [
     ([1] * 130, 0, 0, 256, 256),
     ([5] * 70 + [0] * 900 + [90] * 3, 0, 0, 144, 128),
     ([2500], 0, 0, 7168, 256),
+    ([3000, 0, 4000, 1, 2999], 0, 7, 2064, 400),
+    ([70] * 69 + [0], 0, 3, 1040, 272),
 ]
 
 
@@ -239,7 +241,8 @@ def test_expert_offsets_out_of_order(ep, bad):
 @pytest.mark.parametrize("save", [False, True])
 @pytest.mark.parametrize("counts,before,behind,I,K", [
     ([1], 0, 0, 128, 16), ([0, 3, 20, 0], 1, 2, 256, 208), ([40, 0, 65], 0, 3, 384, 336),
-    ([300, 5, 0, 600], 2, 1, 256, 1040), ([1500], 0, 0, 1408, 512)])
+    ([300, 5, 0, 600], 2, 1, 256, 1040), ([1500], 0, 0, 1408, 512),
+    ([2000, 0, 1500, 700], 0, 5, 2816, 400), ([70] * 66, 0, 0, 512, 144)])
 def test_expert_swiglu(ep, counts, before, behind, I, K, save):
     E, S = len(counts), sum(counts) + before + behind
     say(f"expert swiglu E={E} S={S} I={I} K={K} save={save}")
