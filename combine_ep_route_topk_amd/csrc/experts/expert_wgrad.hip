@@ -2,156 +2,511 @@
 //
 // For expert e with rows [b, n):  dW[e][i][j] = sum_{s in [b, n)} dy[s][i] x[s][j]
 // in f32, stored or added.  The summed axis is the slow one of both operands:
-// tiles of kRows rows are staged as they lie in memory (direct loads into LDS)
-// and the matrix instruction's operands -- eight summed values of one column --
-// come from LDS through its transposing 16-bit read.  A lane ends up with four
-// neighbouring j of one i: 16-byte stores.  Rows past the segment lie outside
-// the load descriptors and read as zero.
+// rows are staged as they lie in memory (direct loads into LDS) and the matrix
+// instruction's operands -- eight summed values of one column -- come from LDS
+// through its transposing 16-bit read.  x is the row operand: a lane ends up
+// with four neighbouring j of one i, 16-byte stores.  Rows past the segment lie
+// outside the load descriptors and read as zero.
 #include "experts_internal.h"
 
 namespace ep {
 namespace {
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-
-constexpr int kRows = 32;                   // summed rows per step: one matrix instruction
 
 struct WgradArgs {
     const uint16_t* dy;
     const uint16_t* x;
     const int32_t* offsets;
-    int S, N, K, E, accumulate;
+    int S, N, K, E;
     float* dw;
 };
 
+__device__ __forceinline__ bf16x8 join(s16x4 lo, s16x4 hi) {
+    return __builtin_bit_cast(
+        bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+}
 
-template <int TN, int TK, int WN, int WK>
-__global__ __launch_bounds__(WN* WK* kWave) void expert_wgrad_kernel(WgradArgs p)
+// Store of four neighbouring j, or their addition to what is there.  A store is
+// issued whatever the tile's edges (the descriptor drops what lies outside).
+template <bool ACC>
+__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
+    if (ACC) {
+        const f32x4 o =
+            __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, int(at), 0, 0));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] += o[c];
+    }
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, int(at), 0, 0);
+}
+
+// A wave's 32 x 32 fragment (lane: column i = lane % 32, rows j in registers) to
+// rows i of 32 j in memory: through `buf`, 4 KB of LDS of the wave's own, so
+// that every store writes eight whole 128-byte lines (straight from registers a
+// lane pair writes 32 bytes of a line: 16 experts x 2816 x 4096 from 128 rows each
+// 230 us, through LDS 163).  Rows of 128 bytes, chunk c of row r at c ^ r % 8.
+template <bool ACC>
+__device__ __forceinline__ void put_fragment(__amdgpu_buffer_rsrc_t r, uint8_t* buf, int lane,
+                                             const f32x16& v, int i0, int j0, int K) {
+    const int lt = lane & 31, lk = lane >> 5;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(buf + lt * 128 + (((2 * q + lk) ^ (lt & 7)) * 16)) =
+            f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();
+    const int row = lane / 8, j = j0 + lane % 8 * 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const f32x4 o = *reinterpret_cast<const f32x4*>(buf + (k * 8 + row) * 128 +
+                                                        (((lane & 7) ^ row) * 16));
+        const int i = i0 + k * 8 + row;
+        put4<ACC>(r, j < K ? (uint32_t(i) * uint32_t(K) + uint32_t(j)) * 4u : kOutside, o);
+    }
+    __builtin_amdgcn_wave_barrier();
+}
+
+// ------------------------------------------------------------- large tiles
+// A persistent workgroup of four waves makes 256 i x 256 j at a time, each wave
+// 128 x 128 with 32 x 32 x 16 matrix instructions (the tile and the reasons of
+// the grouped 8-bit product: 2048 cycles of matrix work for each 64 rows
+// against 1536 of LDS).  64 rows are a step; its 512-byte row parts go through
+// three stages of dy and two of x, all 160 KB of LDS.  A quarter step works on
+// fragments in registers and reads the next quarter's.  Before the last quarter
+// all waves meet: this step's stages have been read, the next step's have
+// landed.  The stream runs on across tiles.
+//
+// Measured on MI355X, 8 experts x 4096 x 7168, 4096 rows each: 1557 us (1.24
+// PFLOP/s; a library product with the same transposed operands 1.11, with both
+// operands the convenient way round 1.44); eight waves of 128 x 64 on two stages,
+// without the units' exchange, 3721 us, all of it LDS bank conflicts.
+//
+// LDS image of a stage: rows of 512 bytes in units of 64, unit u of row r at
+// u ^ r % 4: a transposing read takes 8 rows x 64 bytes, rows 0..3 and 8..11 of
+// 16, which then touch every bank twice, the least that 512 bytes can.
+constexpr int kTile = 256, kRows = 64;
+constexpr int kStage = kRows * kTile * 2;            // 32 KB of one operand
+constexpr int kLoads = kStage / 16 / 256;            // 8 of 16 bytes a thread
+
+template <int VM>
+__device__ __forceinline__ void wait_and_barrier() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+__device__ __forceinline__ void pin(f32x16& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+a"(v));
+#endif
+}
+__device__ __forceinline__ void hide(int& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(v));
+#endif
+}
+
+struct WgradTile {
+    int expert, i0, j0, begin, end;      // expert -1: none
+};
+
+template <bool ACC>
+__global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
 {
-    constexpr int kWaves = WN * WK;
-    constexpr int FN = TN / WN / 16, FK = TK / WK / 16;
-    constexpr int kStage = kRows * (TN + TK) * 2;
-    constexpr int kVecN = TN / 8, kVecK = TK / 8;         // 16-byte vectors of a row
-    constexpr int kLoadsN = kRows * kVecN / kWave / kWaves, kLoadsK = kRows * kVecK / kWave / kWaves;
-    static_assert(kLoadsN * kWave * kWaves == kRows * kVecN, "whole loads");
-    static_assert(kLoadsK * kWave * kWaves == kRows * kVecK, "whole loads");
-    __shared__ __attribute__((aligned(128))) uint8_t lds[2 * kStage];
+    __shared__ __attribute__((aligned(256))) uint8_t lds[5 * kStage];
+    uint8_t* const xstage = lds + 3 * kStage;
 
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wn = wave % WN, wk = wave / WN;
+    const int wi = wave & 1, wj = wave >> 1;
     const int N = p.N, K = p.K;
-    const int nt = (N + TN - 1) / TN, kt = (K + TK - 1) / TK;
-    const int per_expert = nt * kt;
-    const int e = int(blockIdx.x) / per_expert;
-    const int in = int(blockIdx.x) - e * per_expert;
-    const int n0 = in % nt * TN, k0 = in / nt * TK;
-    int begin, end;
-    segment_of(p.offsets, e, p.S, begin, end);
-    begin = __builtin_amdgcn_readfirstlane(begin);
-    end = __builtin_amdgcn_readfirstlane(end);
-    const int rows = end - begin, steps = (rows + kRows - 1) / kRows;
+    const int nt = (N + kTile - 1) / kTile, kt = (K + kTile - 1) / kTile;
+    const int total = nt * kt * p.E;
 
-    uint32_t noff[kLoadsN], koff[kLoadsK];
-#pragma unroll
-    for (int i = 0; i < kLoadsN; ++i) {
-        const int v = (i * kWaves + wave) * kWave + lane, r = v / kVecN, c = n0 + v % kVecN * 8;
-        noff[i] = c < N ? uint32_t(r) * uint32_t(N) * 2u + uint32_t(c) * 2u : kOutside;
-    }
-#pragma unroll
-    for (int i = 0; i < kLoadsK; ++i) {
-        const int v = (i * kWaves + wave) * kWave + lane, r = v / kVecK, c = k0 + v % kVecK * 8;
-        koff[i] = c < K ? uint32_t(r) * uint32_t(K) * 2u + uint32_t(c) * 2u : kOutside;
-    }
-    auto issue = [&](int step) {
-        uint8_t* st = lds + (step & 1) * kStage;
-        const int64_t r0 = begin + int64_t(step) * kRows;
-        const int left = end - int(r0) < kRows ? end - int(r0) : kRows;
-        const __amdgpu_buffer_rsrc_t nr =
-            buffer_rsrc(const_cast<uint16_t*>(p.dy) + r0 * N, int64_t(left) * N * 2);
-        const __amdgpu_buffer_rsrc_t kr =
-            buffer_rsrc(const_cast<uint16_t*>(p.x) + r0 * K, int64_t(left) * K * 2);
-#pragma unroll
-        for (int i = 0; i < kLoadsN; ++i)
-            load16_to_lds(nr, st + (i * kWaves + wave) * 1024, noff[i]);
-#pragma unroll
-        for (int i = 0; i < kLoadsK; ++i)
-            load16_to_lds(kr, st + kRows * TN * 2 + (i * kWaves + wave) * 1024, koff[i]);
+    // Tiles in blocks of as many as an XCD runs at once, given to the XCDs in
+    // turn (experts differ in rows, so a contiguous share each would not do);
+    // within an expert, 8 i tiles x all j tiles, i fastest.
+    const int slots = int(gridDim.x / 8);
+    auto tile_at = [&](int turn) {
+        WgradTile t{-1, 0, 0, 0, 0};
+        const int id = (turn * 8 + int(blockIdx.x % 8)) * slots + int(blockIdx.x / 8);
+        if (id >= total) return t;
+        t.expert = id / (nt * kt);
+        const int in = id - t.expert * nt * kt;
+        const int group = in / (8 * kt), size = nt - group * 8 < 8 ? nt - group * 8 : 8;
+        const int rest = in - group * 8 * kt;
+        t.i0 = (group * 8 + rest % size) * kTile;
+        t.j0 = rest / size * kTile;
+        int b, n;
+        segment_of(p.offsets, t.expert, p.S, b, n);
+        t.begin = __builtin_amdgcn_readfirstlane(b);
+        t.end = __builtin_amdgcn_readfirstlane(n);
+        return t;
     };
-
-    f32x4 acc[FK][FN];
-#pragma unroll
-    for (int i = 0; i < FK; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    // 16 columns from `col` on, all kRows rows: lane group g takes rows 8 g ..
-    const int g = lane / 16, l = lane % 16;
-    auto fragment = [&](uint8_t* base, int C, int col) {
-        uint8_t* a = base + ((g * 8 + l / 4) * C + col + l % 4 * 4) * 2;
-        const s16x4 lo = read_transposed(a);
-        const s16x4 hi = read_transposed(a + 4 * C * 2);
-        const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        return __builtin_bit_cast(bf16x8, v);
+    const int turns = (total + int(gridDim.x) - 1) / int(gridDim.x);
+    auto output = [&](const WgradTile& t) {
+        const int rows = N - t.i0 < kTile ? N - t.i0 : kTile;
+        return buffer_rsrc(p.dw + (int64_t(t.expert) * N + t.i0) * K, int64_t(rows) * K * 4);
     };
-
-    if (steps) issue(0);
-    for (int s = 0; s < steps; ++s) {
-        wait_own_stores();      // this wave's loads into LDS have landed
-        __syncthreads();
-        if (s + 1 < steps) issue(s + 1);
-        uint8_t* st = lds + (s & 1) * kStage;
-        bf16x8 dy[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) dy[j] = fragment(st, TN, (wn * FN + j) * 16);
-#pragma unroll
-        for (int i = 0; i < FK; ++i) {
-            const bf16x8 x = fragment(st + kRows * TN * 2, TK, (wk * FK + i) * 16);
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, dy[j], acc[i][j], 0, 0, 0);
-        }
-    }
-
-    float* out = p.dw + int64_t(e) * N * K;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const int n = n0 + (wn * FN + j) * 16 + l;
-        if (n >= N) continue;
-#pragma unroll
-        for (int i = 0; i < FK; ++i) {
-            const int k = k0 + (wk * FK + i) * 16 + g * 4;
-            if (k >= K) continue;
-            f32x4* d = reinterpret_cast<f32x4*>(out + int64_t(n) * K + k);
-            f32x4 v = acc[i][j];
-            if (p.accumulate) {
-                const f32x4 o = *d;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] += o[c];
+    // tiles without rows: zeros, apart from the stream
+    if (!ACC) {
+        for (int turn = 0; turn < turns; ++turn) {
+            const WgradTile t = tile_at(turn);
+            if (t.expert < 0 || t.end > t.begin) continue;
+            const __amdgpu_buffer_rsrc_t r = output(t);
+            for (int v = threadIdx.x; v < kTile * kTile / 4; v += 256) {
+                const int i = v / (kTile / 4), j = t.j0 + v % (kTile / 4) * 4;
+                put4<false>(r, j < K ? (uint32_t(i) * uint32_t(K) + uint32_t(j)) * 4u : kOutside,
+                            f32x4{0, 0, 0, 0});
             }
-            *d = v;
         }
+    }
+    int turn = 0;
+    auto next_tile = [&]() {       // the next tile with rows
+        WgradTile t{-1, 0, 0, 0, 0};
+        while (turn < turns) {
+            t = tile_at(turn++);
+            if (t.expert < 0 || t.end > t.begin) break;
+            t.expert = -1;
+        }
+        return t;
+    };
+    auto steps_of = [](const WgradTile& t) {     // even: an odd count's last step is zeros
+        return ((t.end - t.begin + kRows - 1) / kRows + 1) & ~1;
+    };
+
+    // One operand's loads of one step: a load instruction fills two rows; its
+    // lanes fetch the chunks that belong there.
+    const int chunk = (lane & 3) | ((((lane >> 2) & 7) ^ ((wave & 1) * 2 + (lane >> 5))) << 2);
+    const int lrow = wave * 2 + lane / 32;
+    struct Source {
+        __amdgpu_buffer_rsrc_t r;
+        uint32_t off, group;
+    };
+    auto source = [&](const uint16_t* base, int width, const WgradTile& t, int c0, int s) {
+        const int64_t row = t.begin + int64_t(s) * kRows;
+        const int64_t left = t.end - row;
+        int c = c0 + chunk * 8;
+        hide(c);          // or every load's offset would take a register of its own
+        const uint32_t off = (uint32_t(lrow) * uint32_t(width) + uint32_t(c)) * 2u;
+        const int64_t use = left <= 0 ? 0 : left < kRows ? left : kRows;
+        return Source{buffer_rsrc(const_cast<uint16_t*>(base) + (use ? row * width : 0),
+                                  use * width * 2),
+                      c < width ? off : kOutside, uint32_t(width) * 16u};
+    };
+    auto issue = [&](const Source& c, uint8_t* to, int i) {
+        load16_to_lds(c.r, to + wave * 1024 + i * 4096, c.off + uint32_t(i) * c.group);
+    };
+
+    // Fragment f of 32 columns, quarter q: two transposing reads of rows
+    // 16 q + 8 (lane / 32) .. + 3 and the four after them.
+    const int g = lane >> 4, l = lane & 15;
+    int foff[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+        foff[f] = ((g >> 1) * 8 + (l >> 2)) * 512 + (f ^ (l >> 2)) * 64 + (g & 1) * 32 + (l & 3) * 8;
+    struct Quarter {
+        s16x4 y[4][2], x[4][2];
+    };
+    auto read = [&](uint8_t* ys, uint8_t* xs, int q, Quarter& f, int n) {
+        const int c = n & 1, i = n >> 1;
+        const int at = q * 16 * 512 + c * 4 * 512;
+        if (i == 0) f.x[0][c] = read_transposed(xs + foff[0] + at);
+        else if (i < 5) f.y[i - 1][c] = read_transposed(ys + foff[i - 1] + at);
+        else f.x[i - 4][c] = read_transposed(xs + foff[i - 4] + at);
+    };
+    f32x16 acc[4][4];      // [j fragment][i fragment]
+    // 16 matrix instructions, between them the reads of the next quarter and
+    // `loads` of eight loads from `first` on into `to`.  The stages are named
+    // restrict: the compiler would wait for every load into LDS before a
+    // transposing read otherwise.
+    auto multiply = [&](const Quarter& f, uint8_t* __restrict__ ys, uint8_t* __restrict__ xs, int q,
+                        Quarter& next, const Source& src, uint8_t* __restrict__ to, int first,
+                        int loads) {
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+            const int a = n / 4, b = n % 4;
+            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                join(f.x[a][0], f.x[a][1]), join(f.y[b][0], f.y[b][1]), acc[a][b], 0, 0, 0);
+            pin(acc[a][b]);
+            read(ys, xs, q, next, n);
+            if (loads && n % (16 / loads) == 16 / loads - 1) issue(src, to, first + n / (16 / loads));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    WgradTile t = next_tile();
+    if (t.expert < 0) return;
+    int steps = steps_of(t);
+    {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Source y = source(p.dy, N, t, t.i0, k), x = source(p.x, K, t, t.j0, k);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) issue(y, lds + k * kStage, i);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) issue(x, xstage + k * kStage, i);
+        }
+    }
+    wait_and_barrier<2 * kLoads>();
+    uint8_t* const yfrag = lds + wi * 256;
+    uint8_t* const xfrag = xstage + wj * 256;
+    Quarter f0, f1;
+#pragma unroll
+    for (int n = 0; n < 16; ++n) read(yfrag, xfrag, 0, f0, n);
+    int yslot = 0;
+    bool stored = false;
+    for (;;) {
+        const WgradTile tnext = next_tile();
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) acc[a][b][c] = 0.0f;
+        for (int s = 0; s < steps; ++s) {
+            const int ynext = yslot == 2 ? 0 : yslot + 1, ylast = yslot == 0 ? 2 : yslot - 1;
+            const bool over = s + 2 >= steps;
+            const int s2 = over ? s + 2 - steps : s + 2;
+            const WgradTile& from = over ? tnext : t;
+            uint8_t* const ys = yfrag + yslot * kStage;
+            uint8_t* const xs = xfrag + (s & 1) * kStage;
+            // dy's stage that step s - 1 left takes step s + 2
+            const Source ysrc = source(p.dy, N, from, from.i0, s2);
+            uint8_t* const yto = lds + ylast * kStage;
+            multiply(f0, ys, xs, 1, f1, ysrc, yto, 0, 4);
+            multiply(f1, ys, xs, 2, f0, ysrc, yto, 4, 4);
+            multiply(f0, ys, xs, 3, f1, ysrc, yto, 0, 0);
+            // newer than the next step's loads: dy's 8, and in a tile's first
+            // step the 64 stores of the last tile
+            if (s == 0 && stored) wait_and_barrier<63>();
+            else wait_and_barrier<kLoads>();
+            __builtin_amdgcn_sched_barrier(0);
+            const Source xsrc = source(p.x, K, from, from.j0, s2);
+            multiply(f1, yfrag + ynext * kStage, xfrag + ((s + 1) & 1) * kStage, 0, f0, xsrc,
+                     xstage + (s & 1) * kStage, 0, 8);
+            yslot = ynext;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // the stage of dy that the last step left is free until the next step
+        // loads into it
+        int el = lane;
+        hide(el);          // keeps the addresses out of the main loop's registers
+        uint8_t* const buf = lds + (yslot == 0 ? 2 : yslot - 1) * kStage + wave * 8192;
+        const __amdgpu_buffer_rsrc_t r = output(t);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                put_fragment<ACC>(r, buf + (a & 1) * 4096, el, acc[a][b], wi * 128 + b * 32,
+                                  t.j0 + wj * 128 + a * 32, K);
+        __syncthreads();
+        if (tnext.expert < 0) break;
+        t = tnext;
+        steps = steps_of(t);
+        stored = !ACC;
+    }
+    wait_and_barrier<0>();          // no load into LDS outlives the workgroup
+}
+
+// ------------------------------------------------------------- small tiles
+// 128 i x 128 j, four waves of 64 x 64, steps of 32 rows on three stages (48 KB:
+// three workgroups a CU, one's stores behind another's loads).  With few tiles
+// each expert's rows are split over `parts` workgroups a tile, whose sums go to
+// a workspace [part][E][N][K] and are joined in order by a second launch.
+constexpr int kSmallTile = 128, kSmallRows = 32;
+constexpr int kSmallStage = 2 * kSmallRows * kSmallTile * 2;      // dy, then x: 16 KB
+
+template <bool ACC>
+__global__ __launch_bounds__(256) void expert_wgrad_small_kernel(WgradArgs p, int parts)
+{
+    constexpr int kStages = 3, kOperand = kSmallStage / 2, kPer = kOperand / 16 / 256;   // 2 loads
+    __shared__ __attribute__((aligned(256))) uint8_t lds[kStages * kSmallStage];
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wi = wave & 1, wj = wave >> 1;
+    const int N = p.N, K = p.K;
+    const int nt = (N + kSmallTile - 1) / kSmallTile, kt = (K + kSmallTile - 1) / kSmallTile;
+    const int part = int(blockIdx.x) % parts, tile = int(blockIdx.x) / parts;
+    const int e = tile / (nt * kt), in = tile - e * nt * kt;
+    const int i0 = in % nt * kSmallTile, j0 = in / nt * kSmallTile;
+    int b0, n0;
+    segment_of(p.offsets, e, p.S, b0, n0);
+    int begin = __builtin_amdgcn_readfirstlane(b0), end = __builtin_amdgcn_readfirstlane(n0);
+    if (ACC && end == begin) return;
+    if (parts > 1) {      // whole steps to each part
+        const int all = (end - begin + kSmallRows - 1) / kSmallRows;
+        const int per = (all + parts - 1) / parts * kSmallRows;
+        const int64_t from = begin + int64_t(part) * per;
+        begin = from < end ? int(from) : end;
+        end = end - begin < per ? end : begin + per;
+    }
+    const int steps = (end - begin + kSmallRows - 1) / kSmallRows;
+
+    // a load instruction fills four rows of 256 bytes in units of 64, unit u of
+    // row r at u ^ r % 4
+    const int lrow = lane / 16, chunk = (lane & 3) | ((((lane >> 2) & 3) ^ (lrow & 3)) << 2);
+    auto issue = [&](int s) {
+        uint8_t* st = lds + s % kStages * kSmallStage;
+        const int64_t row = begin + int64_t(s) * kSmallRows;
+        const int64_t left = end - row, use = left <= 0 ? 0 : left < kSmallRows ? left : kSmallRows;
+        const __amdgpu_buffer_rsrc_t yr =
+            buffer_rsrc(const_cast<uint16_t*>(p.dy) + (use ? row * N : 0), use * N * 2);
+        const __amdgpu_buffer_rsrc_t xr =
+            buffer_rsrc(const_cast<uint16_t*>(p.x) + (use ? row * K : 0), use * K * 2);
+        const int i = i0 + chunk * 8, j = j0 + chunk * 8;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const uint32_t r = (k * 4 + wave) * 4 + lrow;
+            load16_to_lds(yr, st + (k * 4 + wave) * 1024,
+                          i < N ? (r * uint32_t(N) + uint32_t(i)) * 2u : kOutside);
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const uint32_t r = (k * 4 + wave) * 4 + lrow;
+            load16_to_lds(xr, st + kOperand + (k * 4 + wave) * 1024,
+                          j < K ? (r * uint32_t(K) + uint32_t(j)) * 2u : kOutside);
+        }
+    };
+    const int g = lane >> 4, l = lane & 15;
+    const int frow = ((g >> 1) * 8 + (l >> 2)) * 256 + (g & 1) * 32 + (l & 3) * 8;
+    f32x16 acc[2][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) acc[a][b][c] = 0.0f;
+    auto multiply = [&](uint8_t* __restrict__ ys, uint8_t* __restrict__ xs) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            bf16x8 y[2], x[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                uint8_t* a = ys + q * 16 * 256 + frow + (((wi * 2 + f) ^ (l >> 2)) * 64);
+                uint8_t* b = xs + q * 16 * 256 + frow + (((wj * 2 + f) ^ (l >> 2)) * 64);
+                y[f] = join(read_transposed(a), read_transposed(a + 4 * 256));
+                x[f] = join(read_transposed(b), read_transposed(b + 4 * 256));
+            }
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    acc[a][b] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[a], y[b], acc[a][b], 0, 0, 0);
+        }
+    };
+    issue(0);
+    issue(1);
+    for (int s = 0; s < steps; ++s) {
+        wait_and_barrier<2 * kPer>();        // step s has landed, step s - 1 has been read
+        issue(s + 2);                        // past the end: zeros
+        uint8_t* st = lds + s % kStages * kSmallStage;
+        multiply(st, st + kOperand);
+    }
+    wait_and_barrier<0>();          // every stage has been read, no load is on its way
+    const int rows = N - i0 < kSmallTile ? N - i0 : kSmallTile;
+    const __amdgpu_buffer_rsrc_t r =
+        buffer_rsrc(p.dw + ((int64_t(part) * p.E + e) * N + i0) * K, int64_t(rows) * K * 4);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+            put_fragment<ACC>(r, lds + wave * 8192 + a * 4096, lane, acc[a][b], wi * 64 + b * 32,
+                              j0 + wj * 64 + a * 32, K);
+}
+
+hipError_t launch_large(const WgradArgs& p, int64_t tiles, bool accumulate, hipStream_t s)
+{
+    // one workgroup a CU (it takes all of the LDS), each with its share of tiles
+    const int64_t most = (tiles + 7) / 8 * 8;
+    const int64_t cus = device_cu_count() / 8 * 8;
+    const dim3 grid(uint32_t(most < cus || cus == 0 ? most : cus));
+    if (accumulate) EP_LAUNCH((expert_wgrad_large_kernel<true>), grid, dim3(256), 0, s, p);
+    else EP_LAUNCH((expert_wgrad_large_kernel<false>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <bool ACC>
+__global__ __launch_bounds__(256) void join_parts_kernel(const float* __restrict__ sums, int parts,
+                                                         int64_t vecs, float* __restrict__ dw)
+{
+    for (int64_t v = int64_t(blockIdx.x) * 256 + threadIdx.x; v < vecs;
+         v += int64_t(gridDim.x) * 256) {
+        f32x4 o = {0, 0, 0, 0};
+        if (ACC) o = reinterpret_cast<const f32x4*>(dw)[v];
+        f32x4 t = reinterpret_cast<const f32x4*>(sums)[v];
+        for (int q = 1; q < parts; ++q) {
+            const f32x4 u = reinterpret_cast<const f32x4*>(sums)[q * vecs + v];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) t[c] += u[c];
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = ACC ? o[c] + t[c] : t[c];
+        reinterpret_cast<f32x4*>(dw)[v] = o;
     }
 }
 
-template <int TN, int TK, int WN, int WK>
-hipError_t launch(const WgradArgs& p, hipStream_t s)
+hipError_t launch_small(WgradArgs p, int parts, bool accumulate, float* sums, hipStream_t s)
 {
-    const int64_t grid = int64_t((p.N + TN - 1) / TN) * ((p.K + TK - 1) / TK) * p.E;
-    if (grid * WN * WK * kWave >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-    EP_LAUNCH((expert_wgrad_kernel<TN, TK, WN, WK>), dim3(uint32_t(grid)), dim3(WN * WK * kWave), 0,
-              s, p);
+    const int64_t tiles = int64_t((p.N + kSmallTile - 1) / kSmallTile) *
+                          ((p.K + kSmallTile - 1) / kSmallTile) * p.E;
+    if (tiles * parts * 256 >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+    const dim3 grid{uint32_t(tiles * parts)};
+    float* const dw = p.dw;
+    if (parts > 1) p.dw = sums;
+    if (accumulate && parts == 1)
+        EP_LAUNCH((expert_wgrad_small_kernel<true>), grid, dim3(256), 0, s, p, parts);
+    else
+        EP_LAUNCH((expert_wgrad_small_kernel<false>), grid, dim3(256), 0, s, p, parts);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || parts == 1) return e;
+    const int64_t vecs = int64_t(p.E) * p.N * p.K / 4, want = (vecs + 255) / 256;
+    const dim3 join(uint32_t(want < 4096 ? want : 4096));
+    if (accumulate) EP_LAUNCH((join_parts_kernel<true>), join, dim3(256), 0, s, sums, parts, vecs, dw);
+    else EP_LAUNCH((join_parts_kernel<false>), join, dim3(256), 0, s, sums, parts, vecs, dw);
     return hipGetLastError();
+}
+
+int64_t wgrad_tiles(int N, int K, int E, int tile)
+{
+    return int64_t((N + tile - 1) / tile) * ((K + tile - 1) / tile) * E;
+}
+
+// Large tiles want a whole round of them and rows enough to hide their stores
+// (16 experts x 2816 x 4096, large / small tiles: 64 rows each 156 / 150 us, 128
+// rows 163 / 194; 8 experts x 1024 x 1024, half a round: 35 / 31).
+bool wgrad_large(int S, int N, int K, int E)
+{
+    return wgrad_tiles(N, K, E, kTile) >= 256 && S >= int64_t(96) * E;
 }
 
 }  // namespace
 
+// Parts that an expert's rows are split into: 1, unless there are few small
+// tiles (up to 192, towards 768 workgroups) and rows for several parts of 128.
+// 32768 rows, 256 x 512 (8 tiles): 372 us whole, 37 in 64 parts; 4 experts of 4096
+// rows, 512 x 512 (64 tiles): 54, 29 in 12; 8 of 4096, 512 x 1024 (256): 61, 70 in 3.
+// From sizes alone, so that a workspace's size holds on every device.
+int wgrad_parts(int S, int N, int K, int E)
+{
+    if (wgrad_large(S, N, K, E)) return 1;
+    const int64_t tiles = wgrad_tiles(N, K, E, kSmallTile);
+    if (tiles > 192) return 1;
+    const int64_t most = 768 / tiles, rows = S / (int64_t(128) * E);
+    const int64_t parts = most < rows ? most : rows;
+    return parts < 2 ? 1 : parts > 64 ? 64 : int(parts);
+}
+
 hipError_t launch_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32_t* offsets,
                                int S, int N, int K, int E, int accumulate, float* grad_w,
-                               hipStream_t s)
+                               float* sums, hipStream_t s)
 {
-    const WgradArgs p{grad_y, x, offsets, S, N, K, E, accumulate, grad_w};
-    return launch<256, 256, 4, 2>(p, s);
+    const WgradArgs p{grad_y, x, offsets, S, N, K, E, grad_w};
+    if (wgrad_tiles(N, K, E, kSmallTile) >= (int64_t(1) << 30)) return hipErrorInvalidConfiguration;
+    if (wgrad_large(S, N, K, E))
+        return launch_large(p, wgrad_tiles(N, K, E, kTile), accumulate != 0, s);
+    return launch_small(p, sums ? wgrad_parts(S, N, K, E) : 1, accumulate != 0, sums, s);
 }
 
 }  // namespace ep

@@ -150,9 +150,16 @@ ep_status ep_expert_swiglu_fp8(const uint8_t* a, const uint8_t* a_scale, const u
                     fn);
 }
 
+size_t ep_expert_wgrad_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t E)
+{
+    if (S < 1 || N < 8 || K < 8 || E < 1) return 0;
+    const int parts = ep::wgrad_parts(S, N, K, E);
+    return parts > 1 ? size_t(parts) * E * N * K * sizeof(float) : 0;
+}
+
 ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32_t* expert_offsets,
                           int32_t S, int32_t N, int32_t K, int32_t E, int32_t accumulate,
-                          float* grad_w, void* stream)
+                          float* grad_w, void* workspace, size_t workspace_bytes, void* stream)
 {
     const char* fn = "ep_expert_wgrad";
     TimingScope timing_scope;
@@ -163,8 +170,16 @@ ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32
     }
     EP_REQUIRE_PTR(fn, expert_offsets, 4);
     EP_REQUIRE_PTR(fn, grad_w, 16);
+    const size_t need = ep_expert_wgrad_workspace_bytes(S, N, K, E);
+    if (workspace) {
+        EP_REQUIRE_ALIGNED(fn, workspace, 256);
+        if (workspace_bytes < need)
+            return fail(EP_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
+                        workspace_bytes, need);
+    }
     return launched(ep::launch_expert_wgrad(grad_y, x, expert_offsets, S, N, K, E,
                                             accumulate ? 1 : 0, grad_w,
+                                            need ? static_cast<float*>(workspace) : nullptr,
                                             static_cast<hipStream_t>(stream)),
                     fn);
 }

@@ -75,7 +75,8 @@ _SIGS = {
     "ep_expert_swiglu_fp8": ([_P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P, _P, _P],
                              ctypes.c_int),
     "ep_swiglu_grad": ([_P, _P, _i32, _i32, _P, _P, _P], ctypes.c_int),
-    "ep_expert_wgrad": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P], ctypes.c_int),
+    "ep_expert_wgrad_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
+    "ep_expert_wgrad": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P, _sz, _P], ctypes.c_int),
     "ep_moe_tokens_workspace_bytes": ([_i32, _i32, _i32], _sz),
     "ep_moe_tokens": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P, _P, _P, _P, _P, _sz, _P],
                       ctypes.c_int),
@@ -707,11 +708,16 @@ def ep_swiglu_grad(grad_h: torch.Tensor, gate_up: torch.Tensor,
     return grad_gate_up, h
 
 
+def ep_expert_wgrad_workspace_bytes(S: int, N: int, K: int, E: int) -> int:
+    return int(_lib.ep_expert_wgrad_workspace_bytes(S, N, K, E))
+
+
 def ep_expert_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch.Tensor,
                     grad_w: torch.Tensor | None = None, accumulate: bool = False,
-                    stream=None) -> torch.Tensor:
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """grad_y bf16 [S][N], x bf16 [S][K], expert_offsets i32 [E+1] -> grad_w f32 [E][N][K];
-    `accumulate` adds to the grad_w passed in."""
+    `accumulate` adds to the grad_w passed in.  Calls that overlap need a `workspace` each (by
+    default every call that needs one gets its own)."""
     S, N = _shape(grad_y, "grad_y", 2)
     K = _shape(x, "x", 2)[1]
     _bits_ok(grad_y, "grad_y")
@@ -726,8 +732,15 @@ def ep_expert_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch
             raise ValueError("accumulate needs the grad_w to add to")
         grad_w = torch.empty((E, N, K), dtype=torch.float32, device=dev)
     _need(grad_w, "grad_w", torch.float32, (E, N, K))
-    _launch(_lib.ep_expert_wgrad, dev, stream, (x, expert_offsets, grad_w), _ptr(grad_y), _ptr(x),
-            _ptr(expert_offsets), S, N, K, E, int(bool(accumulate)), _ptr(grad_w))
+    if workspace is None:
+        need = ep_expert_wgrad_workspace_bytes(S, N, K, E)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8)
+    _launch(_lib.ep_expert_wgrad, dev, stream, (x, expert_offsets, grad_w, workspace),
+            _ptr(grad_y), _ptr(x), _ptr(expert_offsets), S, N, K, E, int(bool(accumulate)),
+            _ptr(grad_w), _ptr(workspace), workspace.numel() if workspace is not None else 0)
     return grad_w
 
 

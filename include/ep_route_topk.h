@@ -511,8 +511,8 @@ ep_status ep_exchange_waves(int32_t N, int32_t* peer);
  * NULL, except that ep_expert_wgrad writes its zeros), E <= 1024, N, K, I <=
  * 2^17 and multiples of 16 (8 where no 8-bit operand is involved); a tile
  * count past the launch limits is EP_ERR_LAUNCH.  Buffers 16-byte aligned,
- * scales any.  No call needs a workspace but ep_moe_tokens; none keeps state,
- * so calls on several streams and captured ones are independent.
+ * scales any.  No call keeps state: calls on several streams and captured ones
+ * are independent as long as they share no output and no workspace.
  *
  * ep_quantize_fp8: rows as they are.
  *   x bf16 [S][H]   q e4m3 [S][H] out   scale u8 [S][ceil(H/128)] out.  H % 16 == 0.
@@ -580,10 +580,16 @@ ep_status ep_swiglu_grad(const uint16_t* grad_h, const uint16_t* gate_up, int32_
  * rows gets zeros (or is left as it was).
  *   grad_y bf16 [S][N], x bf16 [S][K]; N % 8 == K % 8 == 0
  *   grad_w f32 [E][N][K] out.
+ *   workspace  ep_expert_wgrad_workspace_bytes(S, N, K, E) bytes (0 for most
+ *              sizes: only small matrices over many rows are split), 256-byte
+ *              aligned, contents need no initialisation; or NULL: the rows are
+ *              not split, which is slower and sums in another order.  Calls that
+ *              share one must not overlap.
  * ------------------------------------------------------------------------- */
+size_t ep_expert_wgrad_workspace_bytes(int32_t S, int32_t N, int32_t K, int32_t E);
 ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32_t* expert_offsets,
                           int32_t S, int32_t N, int32_t K, int32_t E, int32_t accumulate,
-                          float* grad_w, void* stream);
+                          float* grad_w, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * The whole layer for 1 <= T <= 64 tokens (one decoding step), in two launches:

@@ -80,10 +80,22 @@ def test_gradients(ep):
     refused(ep, "ep_swiglu_grad", (F, F, 4, 16, None, F, None), bad, "grad_gate_up")
     refused(ep, "ep_swiglu_grad", (F, F, 4, 16, F, ODD, None), bad, "aligned")
     assert ep.library().ep_swiglu_grad(None, None, 0, 16, None, None, None) == ep.EP_OK
-    refused(ep, "ep_expert_wgrad", (F, F, F, 4, 12, 16, 2, 0, F, None), bad, "N=12")
-    refused(ep, "ep_expert_wgrad", (F, F, F, 4, 16, 16, 2, 0, None, None), bad, "grad_w")
-    refused(ep, "ep_expert_wgrad", (None, F, F, 4, 16, 16, 2, 0, F, None), bad, "grad_y")
-    refused(ep, "ep_expert_wgrad", (F, F, None, 4, 16, 16, 2, 0, F, None), bad, "expert_offsets")
+    refused(ep, "ep_expert_wgrad", (F, F, F, 4, 12, 16, 2, 0, F, None, 0, None), bad, "N=12")
+    refused(ep, "ep_expert_wgrad", (F, F, F, 4, 16, 16, 2, 0, None, None, 0, None), bad, "grad_w")
+    refused(ep, "ep_expert_wgrad", (None, F, F, 4, 16, 16, 2, 0, F, None, 0, None), bad, "grad_y")
+    refused(ep, "ep_expert_wgrad", (F, F, None, 4, 16, 16, 2, 0, F, None, 0, None), bad, "expert_offsets")
+
+
+def test_wgrad_workspace(ep):
+    query = ep.library().ep_expert_wgrad_workspace_bytes
+    assert query(32768, 4096, 7168, 8) == 0          # many tiles: not split
+    assert query(100, 256, 512, 1) == 0              # few rows
+    need = query(32768, 256, 512, 1)
+    assert need > 0 and need % (256 * 512 * 4) == 0
+    assert query(0, 256, 512, 1) == 0
+    args = lambda ws, n: (F, F, F, 32768, 256, 512, 1, 0, F, ws, n, None)  # noqa: E731
+    refused(ep, "ep_expert_wgrad", args(F, need - 1), ep.EP_ERR_WORKSPACE, "needs")
+    refused(ep, "ep_expert_wgrad", args(P(0x10010), need), ep.EP_ERR_INVALID_ARG, "256")
 
 
 def test_moe_tokens(ep):

@@ -309,7 +309,9 @@ def test_swiglu_grad(ep, S, I):
 
 @pytest.mark.parametrize("counts,before,behind,N,K", [
     ([1], 0, 0, 8, 8), ([0, 3, 0], 1, 2, 72, 136), ([31, 32, 33, 0, 64], 0, 3, 264, 40),
-    ([300, 5, 0, 600], 2, 1, 256, 512), ([1000, 1], 0, 0, 1040, 776), ([2] * 70, 0, 0, 24, 16)])
+    ([300, 5, 0, 600], 2, 1, 256, 512), ([1000, 1], 0, 0, 1040, 776), ([2] * 70, 0, 0, 24, 16),
+    ([5000], 0, 0, 64, 136), ([1, 4000, 0, 333], 3, 2, 136, 264),
+    ([100, 64, 1, 0, 700], 0, 4, 4104, 776), ([0, 3000, 130, 63], 5, 0, 2056, 2312)])
 def test_expert_wgrad(ep, counts, before, behind, N, K):
     E, S = len(counts), sum(counts) + before + behind
     say(f"expert wgrad E={E} S={S} N={N} K={K}")
@@ -332,6 +334,7 @@ def test_expert_wgrad(ep, counts, before, behind, N, K):
     ep.ep_expert_wgrad(dy, x, off, grad_w=acc, accumulate=True)
     torch.cuda.synchronize()
     assert torch.equal(acc, old + dw), "accumulate adds the same sums"
+    assert torch.equal(ep.ep_expert_wgrad(dy, x, off), dw), "a second call gives other bits"
 
 
 def test_expert_wgrad_against_differences(ep):
