@@ -132,7 +132,8 @@ __device__ __forceinline__ void hide(int& v) {
 
 constexpr int kLargeTile = 256;
 
-template <bool GATED>
+// SAVE: gated, and gate_up is wanted.
+template <bool GATED, bool SAVE>
 __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
 {
     constexpr int kTile = kLargeTile, kBK = kScaleBlock;
@@ -352,7 +353,8 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
                                                    0);
         };
         const __amdgpu_buffer_rsrc_t yr = buffer_rsrc(
-            p.y ? p.y + int64_t(row0) * N : p.y, p.y ? int64_t(rows) * N * 2 : 0);
+            GATED && !SAVE ? p.y : p.y + int64_t(row0) * N,
+            GATED && !SAVE ? 0 : int64_t(rows) * N * 2);
         if constexpr (!GATED) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -372,20 +374,28 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
             uint8_t* scratch = lds + (wslot == 0 ? 2 : wslot - 1) * kStage;
             float* part = reinterpret_cast<float*>(scratch);
             const int I = N / 2;
+            if constexpr (SAVE) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int m = wm * 128 + j * 32 + lt;
-                if (p.y) {
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int q = 0; q < 4; q += 2) {
+                            const int m = wm * 128 + j * 32 + lt;
                             const int n = t.n * kScaleBlock + wn * 64 + (i >> 1) * 32 + (i & 1) * I +
                                           8 * (q + lk);
                             store_pair(yr, (uint32_t(m) * uint32_t(N) + uint32_t(n)) * 2u,
                                        acc[i][j], q);
+                            __builtin_amdgcn_sched_barrier(0);
                         }
-                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pin(acc[i][j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int m = wm * 128 + j * 32 + lt;
                 float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -397,6 +407,7 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
                         top = max_finite(top, v);
                     }
                     pin(acc[2 * i][j]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 top = fmaxf(top, __shfl_xor(top, 32, kWave));
                 if (lk == 0) part[wn * 256 + m] = top;
@@ -413,6 +424,7 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
             for (int j = 0; j < 4; ++j) {
                 const int m = wm * 128 + j * 32 + lt;
                 const float inv = pow2(-ex[j]);
+                __builtin_amdgcn_sched_barrier(0);
                 // rows of 128 bytes in words, word c of row m at c ^ m % 32
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -447,6 +459,12 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
         t = tnext;
         cur = next;
         scur = snext;
+        if constexpr (GATED) {
+            // read again rather than held through the epilogue, whose registers
+            // would spill, each reload a wait for every load and store (23 us a tile)
+#pragma unroll
+            for (int n = 0; n < 16; ++n) read(wfrag + wslot * kStage, xfrag, 0, f0, n);
+        }
     }
     wait_and_barrier<0>();          // no load into LDS outlives the workgroup
 }
