@@ -17,20 +17,20 @@
 namespace ep {
 namespace {
 
-// A workgroup makes 32 weight rows a wave (gated: 16 gate rows and their 16 up
+// A workgroup makes ROWS weight rows a wave (gated: 16 gate rows and their 16 up
 // rows; eight waves make one scale block) x up to TM tokens.  Each wave brings its
 // own rows, and its share of the tokens that all waves use, through LDS by direct
 // loads kDepth - 1 steps of 128 k ahead, counted by one wait a step, since loads
 // return in order.  (Straight into registers in the matrix instruction's order,
 // neighbouring lanes are rows apart and every lane of a load is a request of its
 // own: 8 experts x 4096 x 7168, eight rows each, 65 us instead of 44.)
-template <int TM, int WAVES, bool GATED>
+template <int TM, int WAVES, int ROWS, bool GATED>
 __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmArgs p)
 {
-    constexpr int kDepth = 3, kBK = kScaleBlock, TN = 32 * WAVES;
-    constexpr int FM = TM / 16, kXLoads = TM / 8 / WAVES, kWStage = 32 * kBK, kXStage = TM * kBK;
-    static_assert(!GATED || TN == 256, "a gated tile makes one scale block");
-    constexpr int kOps = 4 + kXLoads;               // loads of one step
+    constexpr int kDepth = 3, kBK = kScaleBlock, TN = ROWS * WAVES, NF = ROWS / 16;
+    constexpr int FM = TM / 16, kXLoads = TM / 8 / WAVES, kWStage = ROWS * kBK, kXStage = TM * kBK;
+    static_assert(!GATED || (TN == 256 && ROWS == 32), "a gated tile makes one scale block");
+    constexpr int kOps = ROWS / 8 + kXLoads;               // loads of one step
     constexpr int kPitch = 68;                      // 64 scale bytes of a token, padded
     __shared__ __attribute__((aligned(256)))
     uint8_t lds[kDepth * (WAVES * kWStage + kXStage) + TM * kPitch];
@@ -54,9 +54,9 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
     const int64_t wrows = GATED ? N - first : (N - first < TN ? N - first : TN);
     const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(
         const_cast<uint8_t*>(p.w) + (int64_t(t.expert) * N + first) * K, wrows * K);
-    const uint32_t woff = uint32_t((GATED ? wave * 16 : wave * 32) + lrow) * uint32_t(K);
+    const uint32_t woff = uint32_t((GATED ? wave * 16 : wave * ROWS) + lrow) * uint32_t(K);
     const uint32_t whalf = uint32_t(GATED ? N / 2 : 16) * uint32_t(K);     // to the second fragment
-    int block = GATED ? tile.n : (int(first) + wave * 32) / kScaleBlock;
+    int block = GATED ? tile.n : (int(first) + wave * ROWS) / kScaleBlock;
     block = block < NB ? block : NB - 1;
     const uint8_t* const wsc = p.w_scale + (int64_t(t.expert) * NB + block) * KB;
 
@@ -67,10 +67,10 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
     const __amdgpu_buffer_rsrc_t xsr =
         buffer_rsrc(const_cast<uint8_t*>(p.a_scale) + int64_t(t.row0) * KB, int64_t(rows) * KB);
 
-    // Steps go round from one that differs between workgroups: all of them at the
-    // same k of rows 4096 bytes apart would keep to a few memory channels (64
-    // experts x 1024 x 4096, four rows each: 69 us, 50).
-    const int turn = (int(blockIdx.x) / 8 * 5 + int(blockIdx.x)) % KB;
+    // Steps go round from one that differs between the weights' tiles: all of them at
+    // the same k of rows 4096 bytes apart would keep to a few memory channels (64
+    // experts x 1024 x 4096, four rows each: 69 us, 47).
+    const int turn = (t.expert * 5 + tile.n * 3) % KB;
     auto block_of = [&](int step) {
         const int s = step + turn;
         return s < KB ? s : s - KB;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
     auto load = [&](int step, int d) {
         const int k = step < KB ? block_of(step) * kBK : K;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < ROWS / 8; ++i) {
             const int kc = k + wchunk[i & 1] * 16;
             const uint32_t row = (i & 1) * 8 * uint32_t(K) + (i >> 1) * whalf;
             load16_to_lds(wr, wstage + d * kWStage + i * 1024,
@@ -110,9 +110,9 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    f32x4 acc[2][FM];
+    f32x4 acc[NF][FM];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NF; ++i)
 #pragma unroll
         for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     // lane: row r, chunks g and 4 + g
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
             for (int i = 0; i < 2; ++i)
                 wscale[i] = __builtin_amdgcn_readlane(ws[GATED ? i : 0], s & 63);
             const uint8_t* const ws_now = wstage + d * kWStage;
-            const i32x8 w0 = fragment(ws_now, l), w1 = fragment(ws_now, 16 + l);
+            const i32x8 w0 = fragment(ws_now, l), w1 = fragment(ws_now, ROWS - 16 + l);
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
                 if (j >= used) break;
@@ -152,8 +152,8 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
                 const int scale = scales[r * kPitch + (s & 63)];
                 acc[0][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     w0, x, acc[0][j], 0, 0, 0, wscale[0], 0, scale);
-                acc[1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    w1, x, acc[1][j], 0, 0, 0, wscale[1], 0, scale);
+                if (NF > 1) acc[NF - 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    w1, x, acc[NF - 1][j], 0, 0, 0, wscale[1], 0, scale);
             }
         }
     }
@@ -166,8 +166,8 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
             if (m >= rows) continue;
             uint16_t* row = p.y + int64_t(t.row0 + m) * N;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n = int(first) + wave * 32 + i * 16 + g * 4;
+            for (int i = 0; i < NF; ++i) {
+                const int n = int(first) + wave * ROWS + i * 16 + g * 4;
                 if (n >= N) continue;
                 *reinterpret_cast<u32x2*>(row + n) =
                     u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]),
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
             const int m = j * 16 + l;
-            const f32x4 gate = acc[0][j], up = acc[1][j];
+            const f32x4 gate = acc[0][j], up = acc[NF - 1][j];
             if (p.y && m < rows) {
                 uint16_t* row = p.y + int64_t(t.row0 + m) * N + int(first) + wave * 16 + g * 4;
                 *reinterpret_cast<u32x2*>(row) = u32x2{pack_bf16x2(gate[0], gate[1]),
@@ -229,13 +229,13 @@ uint32_t gemm_tiles(GemmArgs& p, int TM, int TN)
     return grid < (int64_t(1) << 30) ? uint32_t(grid) : 0;
 }
 
-template <int TM, int WAVES, bool GATED>
+template <int TM, int WAVES, int ROWS, bool GATED>
 hipError_t launch_stream(GemmArgs p, hipStream_t s)
 {
-    const uint32_t grid = gemm_tiles(p, TM, 32 * WAVES);
+    const uint32_t grid = gemm_tiles(p, TM, ROWS * WAVES);
     if (!grid || uint64_t(grid) * WAVES * kWave >= (uint64_t(1) << 31))
         return hipErrorInvalidConfiguration;
-    EP_LAUNCH((expert_gemm_stream_kernel<TM, WAVES, GATED>), dim3(grid), dim3(WAVES * kWave), 0, s,
+    EP_LAUNCH((expert_gemm_stream_kernel<TM, WAVES, ROWS, GATED>), dim3(grid), dim3(WAVES * kWave), 0, s,
               p);
     return hipGetLastError();
 }
@@ -262,16 +262,34 @@ hipError_t launch_large(GemmArgs p, hipStream_t s)
 //   16 x 2816 x 4096                     48: 44 / 40 / 52   128: 75 / 50 / 60
 //   1 x 4096 x 4096                    1024: 38 / 40 / 48  2048: 68 / 52 / 51
 //   4 x 2048 x 4096                     256: 30 / 39 / 48   512: 38 / 40 / 49
+// With few rows the weights are read at the rate of the busiest CU, so as near to
+// one workgroup each as can be; us for 256 / 128 / 64 weight rows a workgroup:
+//   16 experts x 2816 x 4096, 30 rows each  36 / 41 / 38
+//   8 x 4096 x 7168, 32 rows                56 / 44 / 45
+//   2 x 4096 x 7168, 8 rows                 29 / 23 / 20
+//   32 x 4096 x 7168, 16 rows              161 / 160 / 165
+// One workgroup a CU has room for 128 rows: where the 32 rows are an average, of 94
+// to 12, 53 us instead of 64.
 template <bool GATED>
 hipError_t launch(const GemmArgs& p, hipStream_t s)
 {
-    auto tiles = [&](int TM) {
+    const int64_t cus = device_cu_count();
+    auto tiles = [&](int TM, int TN) {
         const int64_t mt = (int64_t(p.S) + TM - 1) / TM;
-        return (mt > p.E ? mt : p.E) * ((p.N + 255) / 256);
+        return (mt > p.E ? mt : p.E) * ((p.N + TN - 1) / TN);
     };
-    if (p.S >= int64_t(160) * p.E && tiles(kLargeTile) >= 112) return launch_large<GATED>(p, s);
-    if (p.S > int64_t(48) * p.E && tiles(128) > 128) return launch_stream<128, 8, GATED>(p, s);
-    return launch_stream<64, GATED ? 8 : 4, GATED>(p, s);
+    if (p.S >= int64_t(160) * p.E && tiles(kLargeTile, 256) >= 112) return launch_large<GATED>(p, s);
+    if (p.S > int64_t(48) * p.E && tiles(128, 256) > 128)
+        return launch_stream<128, 8, 32, GATED>(p, s);
+    if constexpr (!GATED) {
+        const int64_t wide = tiles(64, 256);
+        if (wide > cus || wide * 3 < cus * 2) {
+            if (tiles(32, 64) <= cus) return launch_stream<32, 4, 16, false>(p, s);
+            if (tiles(128, 128) <= cus) return launch_stream<128, 4, 32, false>(p, s);
+            return launch_stream<64, 4, 32, false>(p, s);
+        }
+    }
+    return launch_stream<64, 8, 32, GATED>(p, s);
 }
 
 }  // namespace
