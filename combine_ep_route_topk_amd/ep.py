@@ -114,14 +114,17 @@ def ep_abi_version() -> int:
     return _lib.ep_abi_version()
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream, device) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    if stream is None:        # the handle alone: a Stream object takes 2 us to make
+        return _current_stream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple | None = None):
@@ -133,7 +136,7 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple | None = 
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -567,10 +570,10 @@ def _launch(fn, dev, stream, tensors, *args) -> None:
         if t is not None and t.device != dev:
             raise ValueError(f"tensors lie on different devices: {t.device} and {dev}")
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _P(_stream(stream, dev))))
+        _check(fn(*args, _stream(stream, dev)))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _P(_stream(stream, dev))))
+            _check(fn(*args, _stream(stream, dev)))
 
 
 def ep_quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None,
@@ -581,10 +584,12 @@ def ep_quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None,
     dev, nb = x.device, scale_blocks(H)
     if q is None:
         q = torch.empty((S, H), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _need_one_of(q, "q", _FP8, (S, H))
     if scale is None:
         scale = torch.empty((S, nb), dtype=torch.uint8, device=dev)
-    _need_one_of(q, "q", _FP8, (S, H))
-    _need_one_of(scale, "scale", _SCALE, (S, nb))
+    else:
+        _need_one_of(scale, "scale", _SCALE, (S, nb))
     _launch(_lib.ep_quantize_fp8, dev, stream, (q, scale), _ptr(x), S, H, _ptr(q), _ptr(scale))
     return q, scale
 
@@ -599,10 +604,12 @@ def ep_dispatch_fp8(x: torch.Tensor, pos: torch.Tensor, send: torch.Tensor | Non
     dev, nb = x.device, scale_blocks(H)
     if send is None:
         send = torch.empty((T * k, H), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _need_one_of(send, "send", _FP8, (T * k, H))
     if scale is None:
         scale = torch.empty((T * k, nb), dtype=torch.uint8, device=dev)
-    _need_one_of(send, "send", _FP8, (T * k, H))
-    _need_one_of(scale, "scale", _SCALE, (T * k, nb))
+    else:
+        _need_one_of(scale, "scale", _SCALE, (T * k, nb))
     _launch(_lib.ep_dispatch_fp8, dev, stream, (pos, send, scale), _ptr(x), T, H, k, _ptr(pos),
             _ptr(send), _ptr(scale))
     return send, scale
@@ -653,7 +660,8 @@ def ep_expert_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
     dev = a.device
     if y is None:
         y = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
-    _bits_ok(y, "y", (S, N))
+    else:
+        _bits_ok(y, "y", (S, N))
     _launch(_lib.ep_expert_gemm_fp8, dev, stream, (a_scale, w, w_scale, expert_offsets, y),
             _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), S, N, K, E,
             _ptr(y))
@@ -674,12 +682,14 @@ def ep_expert_swiglu_fp8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tens
     dev, I = a.device, N // 2
     if h is None:
         h = torch.empty((S, I), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _need_one_of(h, "h", _FP8, (S, I))
     if h_scale is None:
         h_scale = torch.empty((S, scale_blocks(I)), dtype=torch.uint8, device=dev)
+    else:
+        _need_one_of(h_scale, "h_scale", _SCALE, (S, scale_blocks(I)))
     if gate_up is None and save_gate_up:
         gate_up = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
-    _need_one_of(h, "h", _FP8, (S, I))
-    _need_one_of(h_scale, "h_scale", _SCALE, (S, scale_blocks(I)))
     if gate_up is not None:
         _bits_ok(gate_up, "gate_up", (S, N))
     _launch(_lib.ep_expert_swiglu_fp8, dev, stream,
@@ -699,10 +709,12 @@ def ep_swiglu_grad(grad_h: torch.Tensor, gate_up: torch.Tensor,
     dev = grad_h.device
     if grad_gate_up is None:
         grad_gate_up = torch.empty((S, 2 * I), dtype=gate_up.dtype, device=dev)
+    else:
+        _bits_ok(grad_gate_up, "grad_gate_up", (S, 2 * I))
     if h is None:
         h = torch.empty((S, I), dtype=grad_h.dtype, device=dev)
-    _bits_ok(grad_gate_up, "grad_gate_up", (S, 2 * I))
-    _bits_ok(h, "h", (S, I))
+    else:
+        _bits_ok(h, "h", (S, I))
     _launch(_lib.ep_swiglu_grad, dev, stream, (gate_up, grad_gate_up, h), _ptr(grad_h),
             _ptr(gate_up), S, I, _ptr(grad_gate_up), _ptr(h))
     return grad_gate_up, h
