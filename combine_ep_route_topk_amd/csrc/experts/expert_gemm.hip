@@ -79,7 +79,7 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
     // row's are neighbours: a lane each, where a load for each step would touch a
     // line for each token).
     int ws[GATED ? 2 : 1];
-    auto load_scales = [&](int step) {
+    auto load_scales = [&](int step, auto&& meanwhile) {
         const int b = block_of(step + lane < KB ? step + lane : 0);
 #pragma unroll
         for (int i = 0; i < (GATED ? 2 : 1); ++i) ws[i] = wsc[int64_t(i) * (NB / 2) * KB + b];
@@ -87,6 +87,8 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
 #pragma unroll
         for (int i = 0; i < TM / WAVES; ++i)
             v[i] = __builtin_amdgcn_raw_buffer_load_b8(xsr, (wave * (TM / WAVES) + i) * KB + b, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        meanwhile();
 #pragma unroll
         for (int i = 0; i < TM / WAVES; ++i)
             scales[(wave * (TM / WAVES) + i) * kPitch + lane] = uint8_t(v[i]);
@@ -123,9 +125,10 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
                      int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
     };
 
-    load_scales(0);
+    load_scales(0, [&] {
 #pragma unroll
-    for (int d = 0; d < kDepth - 1; ++d) load(d, d);
+        for (int d = 0; d < kDepth - 1; ++d) load(d, d);
+    });
     for (int s0 = 0; s0 < KB; s0 += kDepth) {
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) {                // past the last step: zeros
@@ -134,7 +137,7 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
             __builtin_amdgcn_sched_barrier(0);
             const int s = s0 + d;
             if ((s & 63) == 0 && s > 0 && s < KB) {
-                load_scales(s);
+                load_scales(s, [] {});
                 __syncthreads();
             }
             load(s + kDepth - 1, (d + kDepth - 1) % kDepth);
