@@ -28,42 +28,56 @@ __device__ __forceinline__ bf16x8 join(s16x4 lo, s16x4 hi) {
         bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 }
 
-// Store of four neighbouring j, or their addition to what is there.  A store is
-// issued whatever the tile's edges (the descriptor drops what lies outside).
-template <bool ACC>
-__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
-    if (ACC) {
-        const f32x4 o =
-            __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, int(at), 0, 0));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] += o[c];
-    }
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, int(at), 0, 0);
-}
-
-// A wave's 32 x 32 fragment (lane: column i = lane % 32, rows j in registers) to
-// rows i of 32 j in memory: through `buf`, 4 KB of LDS of the wave's own, so
-// that every store writes eight whole 128-byte lines (straight from registers a
-// lane pair writes 32 bytes of a line: 16 experts x 2816 x 4096 from 128 rows each
+// The fragments of A x 32 j that a wave holds of 32 i (lane: column i = lane % 32,
+// rows j in registers) to rows i of 32 j in memory, or added to what is there:
+// through `buf`, 4 KB of LDS of the wave's own for each of two fragments, so that
+// every store writes eight whole 128-byte lines (straight from registers a lane
+// pair writes 32 bytes of a line: 16 experts x 2816 x 4096 from 128 rows each
 // 230 us, through LDS 163).  Rows of 128 bytes, chunk c of row r at c ^ r % 8.
-template <bool ACC>
-__device__ __forceinline__ void put_fragment(__amdgpu_buffer_rsrc_t r, uint8_t* buf, int lane,
-                                             const f32x16& v, int i0, int j0, int K) {
-    const int lt = lane & 31, lk = lane >> 5;
+// All A fragments' old values are asked for at once.  A store is issued whatever
+// the tile's edges (the descriptor drops what lies outside).
+//
+// NT: past the caches, so that a large output does not push the operands, which
+// every tile of an expert reads again, out of L2 (128 rows each: 133 us instead of
+// 197; an output that fits, 8 x 1024 x 1024: 33, 28).
+template <bool ACC, bool NT, int A>
+__device__ __forceinline__ void put_fragments(__amdgpu_buffer_rsrc_t r, uint8_t* buf, int lane,
+                                              const f32x16 (&v)[A], int i0, int j0, int K) {
+    const int lt = lane & 31, lk = lane >> 5, row = lane / 8;
+    auto at = [&](int a, int k) {
+        const int i = i0 + k * 8 + row, j = j0 + a * 32 + lane % 8 * 4;
+        return j < K ? (uint32_t(i) * uint32_t(K) + uint32_t(j)) * 4u : kOutside;
+    };
+    f32x4 old[ACC ? A : 1][4];
+    if (ACC) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(buf + lt * 128 + (((2 * q + lk) ^ (lt & 7)) * 16)) =
-            f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-    __builtin_amdgcn_wave_barrier();
-    const int row = lane / 8, j = j0 + lane % 8 * 4;
+        for (int a = 0; a < A; ++a)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const f32x4 o = *reinterpret_cast<const f32x4*>(buf + (k * 8 + row) * 128 +
-                                                        (((lane & 7) ^ row) * 16));
-        const int i = i0 + k * 8 + row;
-        put4<ACC>(r, j < K ? (uint32_t(i) * uint32_t(K) + uint32_t(j)) * 4u : kOutside, o);
+            for (int k = 0; k < 4; ++k)
+                old[a][k] = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, int(at(a, k)), 0, NT ? 2 : 0));
+        __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+        uint8_t* const to = buf + (a & 1) * 4096;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(to + lt * 128 + (((2 * q + lk) ^ (lt & 7)) * 16)) =
+                f32x4{v[a][4 * q], v[a][4 * q + 1], v[a][4 * q + 2], v[a][4 * q + 3]};
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f32x4 o = *reinterpret_cast<const f32x4*>(to + (k * 8 + row) * 128 +
+                                                      (((lane & 7) ^ row) * 16));
+            if (ACC)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[c] += old[a][k][c];
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), r, int(at(a, k)), 0,
+                                                   NT ? 2 : 0);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // ------------------------------------------------------------- large tiles
@@ -125,7 +139,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
 
     // Tiles in blocks of as many as an XCD runs at once, given to the XCDs in
     // turn (experts differ in rows, so a contiguous share each would not do);
-    // within an expert, 8 i tiles x all j tiles, i fastest.
+    // within an expert, 8 j tiles x all i tiles, j fastest.
     const int slots = int(gridDim.x / 8);
     auto tile_at = [&](int turn) {
         WgradTile t{-1, 0, 0, 0, 0};
@@ -133,10 +147,10 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
         if (id >= total) return t;
         t.expert = id / (nt * kt);
         const int in = id - t.expert * nt * kt;
-        const int group = in / (8 * kt), size = nt - group * 8 < 8 ? nt - group * 8 : 8;
-        const int rest = in - group * 8 * kt;
-        t.i0 = (group * 8 + rest % size) * kTile;
-        t.j0 = rest / size * kTile;
+        const int group = in / (8 * nt), size = kt - group * 8 < 8 ? kt - group * 8 : 8;
+        const int rest = in - group * 8 * nt;
+        t.j0 = (group * 8 + rest % size) * kTile;
+        t.i0 = rest / size * kTile;
         int b, n;
         segment_of(p.offsets, t.expert, p.S, b, n);
         t.begin = __builtin_amdgcn_readfirstlane(b);
@@ -156,8 +170,9 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
             const __amdgpu_buffer_rsrc_t r = output(t);
             for (int v = threadIdx.x; v < kTile * kTile / 4; v += 256) {
                 const int i = v / (kTile / 4), j = t.j0 + v % (kTile / 4) * 4;
-                put4<false>(r, j < K ? (uint32_t(i) * uint32_t(K) + uint32_t(j)) * 4u : kOutside,
-                            f32x4{0, 0, 0, 0});
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    u32x4{0, 0, 0, 0}, r,
+                    int(j < K ? (uint32_t(i) * uint32_t(K) + uint32_t(j)) * 4u : kOutside), 0, 2);
             }
         }
     }
@@ -215,7 +230,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
         else if (i < 5) f.y[i - 1][c] = read_transposed(ys + foff[i - 1] + at);
         else f.x[i - 4][c] = read_transposed(xs + foff[i - 4] + at);
     };
-    f32x16 acc[4][4];      // [j fragment][i fragment]
+    f32x16 acc[4][4];      // [i fragment][j fragment]
     // 16 matrix instructions, between them the reads of the next quarter and
     // `loads` of eight loads from `first` on into `to`.  The stages are named
     // restrict: the compiler would wait for every load into LDS before a
@@ -226,9 +241,9 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
             const int a = n / 4, b = n % 4;
-            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                join(f.x[a][0], f.x[a][1]), join(f.y[b][0], f.y[b][1]), acc[a][b], 0, 0, 0);
-            pin(acc[a][b]);
+            acc[b][a] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                join(f.x[a][0], f.x[a][1]), join(f.y[b][0], f.y[b][1]), acc[b][a], 0, 0, 0);
+            pin(acc[b][a]);
             read(ys, xs, q, next, n);
             if (loads && n % (16 / loads) == 16 / loads - 1) issue(src, to, first + n / (16 / loads));
             __builtin_amdgcn_sched_barrier(0);
@@ -296,10 +311,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
         const __amdgpu_buffer_rsrc_t r = output(t);
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-                put_fragment<ACC>(r, buf + (a & 1) * 4096, el, acc[a][b], wi * 128 + b * 32,
-                                  t.j0 + wj * 128 + a * 32, K);
+            put_fragments<ACC, true>(r, buf, el, acc[b], wi * 128 + b * 32, t.j0 + wj * 128, K);
         __syncthreads();
         if (tnext.expert < 0) break;
         t = tnext;
@@ -317,7 +329,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
 constexpr int kSmallTile = 128, kSmallRows = 32;
 constexpr int kSmallStage = 2 * kSmallRows * kSmallTile * 2;      // dy, then x: 16 KB
 
-template <bool ACC>
+template <bool ACC, bool NT>
 __global__ __launch_bounds__(256) void expert_wgrad_small_kernel(WgradArgs p, int parts)
 {
     constexpr int kStages = 3, kOperand = kSmallStage / 2, kPer = kOperand / 16 / 256;   // 2 loads
@@ -329,7 +341,7 @@ __global__ __launch_bounds__(256) void expert_wgrad_small_kernel(WgradArgs p, in
     const int nt = (N + kSmallTile - 1) / kSmallTile, kt = (K + kSmallTile - 1) / kSmallTile;
     const int part = int(blockIdx.x) % parts, tile = int(blockIdx.x) / parts;
     const int e = tile / (nt * kt), in = tile - e * nt * kt;
-    const int i0 = in % nt * kSmallTile, j0 = in / nt * kSmallTile;
+    const int i0 = in / kt * kSmallTile, j0 = in % kt * kSmallTile;
     int b0, n0;
     segment_of(p.offsets, e, p.S, b0, n0);
     int begin = __builtin_amdgcn_readfirstlane(b0), end = __builtin_amdgcn_readfirstlane(n0);
@@ -392,8 +404,8 @@ __global__ __launch_bounds__(256) void expert_wgrad_small_kernel(WgradArgs p, in
             for (int a = 0; a < 2; ++a)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
-                    acc[a][b] =
-                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[a], y[b], acc[a][b], 0, 0, 0);
+                    acc[b][a] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[a], y[b], acc[b][a], 0, 0, 0);
         }
     };
     issue(0);
@@ -410,10 +422,7 @@ __global__ __launch_bounds__(256) void expert_wgrad_small_kernel(WgradArgs p, in
         buffer_rsrc(p.dw + ((int64_t(part) * p.E + e) * N + i0) * K, int64_t(rows) * K * 4);
 #pragma unroll
     for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-            put_fragment<ACC>(r, lds + wave * 8192 + a * 4096, lane, acc[a][b], wi * 64 + b * 32,
-                              j0 + wj * 64 + a * 32, K);
+        put_fragments<ACC, NT>(r, lds + wave * 8192, lane, acc[b], wi * 64 + b * 32, j0 + wj * 64, K);
 }
 
 hipError_t launch_large(const WgradArgs& p, int64_t tiles, bool accumulate, hipStream_t s)
@@ -455,10 +464,14 @@ hipError_t launch_small(WgradArgs p, int parts, bool accumulate, float* sums, hi
     const dim3 grid{uint32_t(tiles * parts)};
     float* const dw = p.dw;
     if (parts > 1) p.dw = sums;
-    if (accumulate && parts == 1)
-        EP_LAUNCH((expert_wgrad_small_kernel<true>), grid, dim3(256), 0, s, p, parts);
-    else
-        EP_LAUNCH((expert_wgrad_small_kernel<false>), grid, dim3(256), 0, s, p, parts);
+    const bool nt = parts == 1 && int64_t(p.E) * p.N * p.K >= int64_t(16) << 20;   // 64 MB
+    if (accumulate && parts == 1) {
+        if (nt) EP_LAUNCH((expert_wgrad_small_kernel<true, true>), grid, dim3(256), 0, s, p, parts);
+        else EP_LAUNCH((expert_wgrad_small_kernel<true, false>), grid, dim3(256), 0, s, p, parts);
+    } else {
+        if (nt) EP_LAUNCH((expert_wgrad_small_kernel<false, true>), grid, dim3(256), 0, s, p, parts);
+        else EP_LAUNCH((expert_wgrad_small_kernel<false, false>), grid, dim3(256), 0, s, p, parts);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1) return e;
     const int64_t vecs = int64_t(p.E) * p.N * p.K / 4, want = (vecs + 255) / 256;
@@ -474,11 +487,11 @@ int64_t wgrad_tiles(int N, int K, int E, int tile)
 }
 
 // Large tiles want a whole round of them and rows enough to hide their stores
-// (16 experts x 2816 x 4096, large / small tiles: 64 rows each 156 / 150 us, 128
-// rows 163 / 194; 8 experts x 1024 x 1024, half a round: 35 / 31).
+// (16 experts x 2816 x 4096, large / small tiles: 128 rows each 145 / 133 us, 176
+// rows 170 / 170, 256 rows 169 / 186; 8 experts x 1024 x 1024, half a round: 35 / 31).
 bool wgrad_large(int S, int N, int K, int E)
 {
-    return wgrad_tiles(N, K, E, kTile) >= 256 && S >= int64_t(96) * E;
+    return wgrad_tiles(N, K, E, kTile) >= 256 && S >= int64_t(192) * E;
 }
 
 }  // namespace

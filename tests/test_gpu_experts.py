@@ -147,6 +147,9 @@ SHAPES = [
     ([2500], 0, 0, 7168, 256),
     ([3000, 0, 4000, 1, 2999], 0, 7, 2064, 400),
     ([70] * 69 + [0], 0, 3, 1040, 272),
+    ([11] * 15 + [100], 0, 0, 2816, 400),
+    ([40, 0, 9], 0, 2, 272, 8464),
+    ([70, 20, 60, 0, 50, 90, 49, 61, 60], 1, 0, 4112, 8320),
 ]
 
 
@@ -242,7 +245,8 @@ def test_expert_offsets_out_of_order(ep, bad):
 @pytest.mark.parametrize("counts,before,behind,I,K", [
     ([1], 0, 0, 128, 16), ([0, 3, 20, 0], 1, 2, 256, 208), ([40, 0, 65], 0, 3, 384, 336),
     ([300, 5, 0, 600], 2, 1, 256, 1040), ([1500], 0, 0, 1408, 512),
-    ([2000, 0, 1500, 700], 0, 5, 2816, 400), ([70] * 66, 0, 0, 512, 144)])
+    ([2000, 0, 1500, 700], 0, 5, 2816, 400), ([70] * 66, 0, 0, 512, 144),
+    ([20, 3], 0, 1, 128, 8336), ([90] * 10, 0, 0, 1792, 8208)])
 def test_expert_swiglu(ep, counts, before, behind, I, K, save):
     E, S = len(counts), sum(counts) + before + behind
     say(f"expert swiglu E={E} S={S} I={I} K={K} save={save}")
@@ -311,7 +315,8 @@ def test_swiglu_grad(ep, S, I):
     ([1], 0, 0, 8, 8), ([0, 3, 0], 1, 2, 72, 136), ([31, 32, 33, 0, 64], 0, 3, 264, 40),
     ([300, 5, 0, 600], 2, 1, 256, 512), ([1000, 1], 0, 0, 1040, 776), ([2] * 70, 0, 0, 24, 16),
     ([5000], 0, 0, 64, 136), ([1, 4000, 0, 333], 3, 2, 136, 264),
-    ([100, 64, 1, 0, 700], 0, 4, 4104, 776), ([0, 3000, 130, 63], 5, 0, 2056, 2312)])
+    ([100, 64, 1, 0, 700], 0, 4, 4104, 776), ([0, 3000, 130, 63], 5, 0, 2056, 2312),
+    ([300, 64, 1, 0, 900], 0, 4, 4104, 776), ([200, 0, 250, 1000], 2, 3, 2056, 4104)])
 def test_expert_wgrad(ep, counts, before, behind, N, K):
     E, S = len(counts), sum(counts) + before + behind
     say(f"expert wgrad E={E} S={S} N={N} K={K}")
@@ -422,6 +427,9 @@ MOE = [(1, 16, 128, 1, 1, True), (1, 7168, 256, 16, 8, True), (3, 208, 128, 8, 2
        (16, 256, 384, 4, 4, True), (17, 272, 256, 5, 3, True), (33, 1040, 128, 12, 6, True),
        (64, 512, 256, 3, 2, True), (64, 256, 128, 70, 8, True),
        (1, 16, 16, 1, 1, False), (2, 4096, 1408, 9, 8, False), (5, 144, 80, 6, 2, False),
+       (2, 8336, 128, 3, 2, True), (2, 256, 8320, 3, 2, True), (1, 8336, 8320, 2, 2, True),
+       (48, 144, 128, 1, 1, True), (9, 528, 128, 20, 12, True), (5, 1040, 256, 3, 3, True),
+       (40, 144, 80, 1, 1, False), (1, 272, 80, 20, 16, False), (3, 8336, 48, 2, 2, False),
        (31, 336, 48, 4, 3, False), (64, 256, 112, 2, 1, False), (64, 128, 64, 64, 64, False)]
 
 
@@ -457,6 +465,20 @@ def test_moe_tokens_picks(ep, fp8):
     idx[:] = -1
     out = ep.ep_moe_tokens(**c)
     torch.cuda.synchronize()
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_moe_one_token_picks(ep, fp8):
+    """One token: picks outside [0, E), an expert picked three times, no pick at all."""
+    c = moe_case(ep, 1, 272, 128, 6, 6, fp8)
+    say(f"moe one token picks fp8={fp8}")
+    for picks in ([3, 3, 0, 3, 5, 0], [-1, 6, 2, 2 ** 31 - 1, -2 ** 31, 2], [-1] * 6):
+        c["topk_idx"][0] = torch.tensor(picks, dtype=torch.int32, device=DEV)
+        out = ep.ep_moe_tokens(**c)
+        torch.cuda.synchronize()
+        want, bound = moe_ref(c)
+        close(out, want, bound, "out")
     assert (out == 0).all()
 
 
