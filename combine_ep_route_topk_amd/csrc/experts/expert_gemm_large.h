@@ -342,36 +342,54 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
         const int row0 = t.rows.row0;
         const int rows = t.rows.end - row0 < kTile ? t.rows.end - row0 : kTile;
         // 16 bf16 of two neighbouring q to one 16-byte store a lane
-        auto store_pair = [&](__amdgpu_buffer_rsrc_t r, uint32_t at, const f32x16& v, int q) {
+        auto pack_pair = [&](const f32x16& v, int q) {
             const auto lo = __builtin_amdgcn_permlane32_swap(
                 pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 4], v[4 * q + 5]), false,
                 false);
             const auto hi = __builtin_amdgcn_permlane32_swap(
                 pack_bf16x2(v[4 * q + 2], v[4 * q + 3]), pack_bf16x2(v[4 * q + 6], v[4 * q + 7]),
                 false, false);
-            __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, r, int(at), 0,
-                                                   0);
+            return u32x4{lo[0], hi[0], lo[1], hi[1]};
         };
         const __amdgpu_buffer_rsrc_t yr = buffer_rsrc(
             GATED && !SAVE ? p.y : p.y + int64_t(row0) * N,
             GATED && !SAVE ? 0 : int64_t(rows) * N * 2);
+        // the weights' stage that the last step left is free until the next step
+        // loads into it
+        uint8_t* const scratch = lds + (wslot == 0 ? 2 : wslot - 1) * kStage;
         if constexpr (!GATED) {
+            // 32 tokens x 128 weight rows at a time through 8 KB of the wave's own,
+            // so that stores write whole lines, past the caches, where tokens and
+            // weights are read again (32-byte parts of lines, straight from
+            // registers: 32768 rows x 7168 x 4096 830 us, so 815): rows of 256
+            // bytes, chunk c of 16 of row r at c ^ r % 16
+            uint8_t* const mine = scratch + wave * 8192;
+            const int srow = lane / 16, sn = t.n * kTile + wn * 128 + lane % 16 * 8;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        const int m = wm * 128 + j * 32 + lt;
-                        const int n = t.n * kTile + wn * 128 + i * 32 + 8 * (q + lk);
-                        store_pair(yr, n < N ? (uint32_t(m) * uint32_t(N) + uint32_t(n)) * 2u
-                                             : kOutside, acc[i][j], q);
-                    }
+                    for (int q = 0; q < 4; q += 2)
+                        *reinterpret_cast<u32x4*>(
+                            mine + lt * 256 + (((i * 4 + q + lk) ^ (lt & 15)) * 16)) =
+                            pack_pair(acc[i][j], q);
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = k * 4 + srow, m = wm * 128 + j * 32 + r;
+                    const u32x4 v = load16(mine + r * 256 + (((lane & 15) ^ (r & 15)) * 16));
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        v, yr,
+                        int(sn < N ? (uint32_t(m) * uint32_t(N) + uint32_t(sn)) * 2u : kOutside), 0,
+                        2);
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+            __syncthreads();        // the scratch is read before the next loads into it
         } else {
-            // the weights' stage that the last step left is free until the next
-            // step loads into it: first the waves' maxima [2][256], then the
-            // tile's 256 x 128 bytes on their way to whole-line stores
-            uint8_t* scratch = lds + (wslot == 0 ? 2 : wslot - 1) * kStage;
+            // the waves' maxima [2][256], then the tile's 256 x 128 bytes on their way
+            // to whole-line stores
             float* part = reinterpret_cast<float*>(scratch);
             const int I = N / 2;
             if constexpr (SAVE) {
@@ -384,8 +402,9 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
                             const int m = wm * 128 + j * 32 + lt;
                             const int n = t.n * kScaleBlock + wn * 64 + (i >> 1) * 32 + (i & 1) * I +
                                           8 * (q + lk);
-                            store_pair(yr, (uint32_t(m) * uint32_t(N) + uint32_t(n)) * 2u,
-                                       acc[i][j], q);
+                            __builtin_amdgcn_raw_buffer_store_b128(
+                                pack_pair(acc[i][j], q), yr,
+                                int((uint32_t(m) * uint32_t(N) + uint32_t(n)) * 2u), 0, 0);
                             __builtin_amdgcn_sched_barrier(0);
                         }
 #pragma unroll
