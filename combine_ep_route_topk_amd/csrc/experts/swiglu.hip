@@ -4,7 +4,11 @@
 //   dg = dh u (sig + silu (1 - sig)),   du = dh silu,   h = silu u.
 // One pass: 3 I values read and 3 I written for each row (h is what the
 // second weight's gradient needs, and recomputing it here costs no extra
-// read).  HBM-bound.  All arithmetic is f32; each output rounds once.
+// read).  All arithmetic is f32; each output rounds once.
+//
+// HBM-bound, nothing is used twice: loads and stores past the caches, one 16-byte
+// piece a thread.  32768 rows of 2048 on MI355X: 130 us, 6.2 TB/s (with a grid of
+// 16 workgroups a CU that goes round: 142; through the caches besides: 152).
 #include "experts_internal.h"
 
 namespace ep {
@@ -19,8 +23,8 @@ __global__ __launch_bounds__(kBlock) void swiglu_grad_kernel(
         const int64_t row = i / rowvecs;
         const int c = int(i - row * rowvecs) * 8;
         const int64_t at = row * 2 * I + c;
-        const u32x4 g = load16(gate_up + at), u = load16(gate_up + at + I);
-        const u32x4 d = load16(grad_h + row * I + c);
+        const u32x4 g = load16_nt(gate_up + at), u = load16_nt(gate_up + at + I);
+        const u32x4 d = load16_nt(grad_h + row * I + c);
         u32x4 dg, du, o;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -39,9 +43,9 @@ __global__ __launch_bounds__(kBlock) void swiglu_grad_kernel(
             du[p] = pack_bf16x2(b[0], b[1]);
             o[p] = pack_bf16x2(hh[0], hh[1]);
         }
-        store16(grad_gate_up + at, dg);
-        store16(grad_gate_up + at + I, du);
-        if (h) store16(h + row * I + c, o);
+        store16_nt(grad_gate_up + at, dg);
+        store16_nt(grad_gate_up + at + I, du);
+        if (h) store16_nt(h + row * I + c, o);
     }
 }
 
@@ -52,8 +56,7 @@ hipError_t launch_swiglu_grad(const uint16_t* grad_h, const uint16_t* gate_up, i
 {
     const int64_t vecs = int64_t(S) * (I / 8);
     const int64_t want = (vecs + kBlock - 1) / kBlock;
-    const uint32_t cap = device_cu_count() * 16;
-    const uint32_t grid = want < int64_t(cap) ? uint32_t(want) : cap;
+    const uint32_t grid = want < (1 << 20) ? uint32_t(want) : 1u << 20;
     EP_LAUNCH(swiglu_grad_kernel, dim3(grid), dim3(kBlock), 0, s, grad_h, gate_up, vecs, I, I / 8,
               grad_gate_up, h);
     return hipGetLastError();
