@@ -24,7 +24,7 @@ namespace {
 // return in order.  (Straight into registers in the matrix instruction's order,
 // neighbouring lanes are rows apart and every lane of a load is a request of its
 // own: 8 experts x 4096 x 7168, eight rows each, 65 us instead of 44.)
-template <int TM, int WAVES, int ROWS, bool GATED>
+template <int TM, int WAVES, int ROWS, bool GATED, bool NT>
 __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmArgs p)
 {
     constexpr int kDepth = 3, kBK = kScaleBlock, TN = ROWS * WAVES, NF = ROWS / 16;
@@ -99,13 +99,13 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
         for (int i = 0; i < ROWS / 8; ++i) {
             const int kc = k + wchunk[i & 1] * 16;
             const uint32_t row = (i & 1) * 8 * uint32_t(K) + (i >> 1) * whalf;
-            load16_to_lds(wr, wstage + d * kWStage + i * 1024,
+            load16_to_lds<NT>(wr, wstage + d * kWStage + i * 1024,
                           kc < K ? woff + row + uint32_t(kc) : kOutside);
         }
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) {
             const int kc = k + xchunk * 16;
-            load16_to_lds(xr, xstage + d * kXStage + (i * WAVES + wave) * 1024,
+            load16_to_lds<false>(xr, xstage + d * kXStage + (i * WAVES + wave) * 1024,
                           kc < K ? xoff + uint32_t(i * WAVES * 8) * uint32_t(K) + uint32_t(kc)
                                  : kOutside);
         }
@@ -238,8 +238,11 @@ hipError_t launch_stream(GemmArgs p, hipStream_t s)
     const uint32_t grid = gemm_tiles(p, TM, ROWS * WAVES);
     if (!grid || uint64_t(grid) * WAVES * kWave >= (uint64_t(1) << 31))
         return hipErrorInvalidConfiguration;
-    EP_LAUNCH((expert_gemm_stream_kernel<TM, WAVES, ROWS, GATED>), dim3(grid), dim3(WAVES * kWave), 0, s,
-              p);
+    const dim3 block(WAVES * kWave);
+    if (int64_t(p.E) * p.N * p.K > kStreamBytes)
+        EP_LAUNCH((expert_gemm_stream_kernel<TM, WAVES, ROWS, GATED, true>), dim3(grid), block, 0, s, p);
+    else
+        EP_LAUNCH((expert_gemm_stream_kernel<TM, WAVES, ROWS, GATED, false>), dim3(grid), block, 0, s, p);
     return hipGetLastError();
 }
 

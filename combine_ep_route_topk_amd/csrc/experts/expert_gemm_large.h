@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
                       uint32_t(off) | (lchunk * 16 >= left ? kOutside : 0), to + wave * 1024};
     };
     auto issue = [&](const Source& c, bool weights, int i) {
-        load16_to_lds(c.r, c.to + i * 4096, c.off + (weights ? weight_group(i) : token_group(i)));
+        load16_to_lds<false>(c.r, c.to + i * 4096, c.off + (weights ? weight_group(i) : token_group(i)));
     };
 
     // scale bytes of one 128-block: the wave's 128 weight rows share one (gated:

@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
                       c < width ? off : kOutside, uint32_t(width) * 16u};
     };
     auto issue = [&](const Source& c, uint8_t* to, int i) {
-        load16_to_lds(c.r, to + wave * 1024 + i * 4096, c.off + uint32_t(i) * c.group);
+        load16_to_lds<false>(c.r, to + wave * 1024 + i * 4096, c.off + uint32_t(i) * c.group);
     };
 
     // Fragment f of 32 columns, quarter q: two transposing reads of rows
@@ -370,13 +370,13 @@ __global__ __launch_bounds__(256) void expert_wgrad_small_kernel(WgradArgs p, in
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const uint32_t r = (k * 4 + wave) * 4 + lrow;
-            load16_to_lds(yr, st + (k * 4 + wave) * 1024,
+            load16_to_lds<false>(yr, st + (k * 4 + wave) * 1024,
                           i < N ? (r * uint32_t(N) + uint32_t(i)) * 2u : kOutside);
         }
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const uint32_t r = (k * 4 + wave) * 4 + lrow;
-            load16_to_lds(xr, st + kOperand + (k * 4 + wave) * 1024,
+            load16_to_lds<false>(xr, st + kOperand + (k * 4 + wave) * 1024,
                           j < K ? (r * uint32_t(K) + uint32_t(j)) * 2u : kOutside);
         }
     };

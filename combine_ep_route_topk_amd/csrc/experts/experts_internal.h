@@ -81,10 +81,18 @@ __device__ __forceinline__ float sigmoid(float g) {
 // ----------------------------------------------------------------- LDS
 // 16 bytes per lane from offset `off` of the descriptor straight into LDS at
 // `to` (wave-uniform) + 16 * lane; an offset past the descriptor stores zeros.
+// NT: past the caches.
+template <bool NT>
 __device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(to), 16,
-                                             int(off), 0, 0, 0);
+                                             int(off), 0, 0, NT ? 2 : 0);
 }
+// Weights that one call reads once, of more than this, are read past the caches:
+// until their next use the rest of a model will have gone through the 256 MB that
+// the memory side keeps.  Streaming weights on MI355X, cached / past the caches: 235
+// MB (8 experts x 4096 x 7168, 32 rows each) 43 / 39 us, 940 MB 159 / 145; 33 MB
+// that the last call left there 11 / 15.
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
 constexpr uint32_t kOutside = 0x80000000u;   // past every descriptor used here
 
 // Transposing read: the 16 lanes of a group read 4 rows x 16 columns of 16-bit

@@ -17,7 +17,9 @@
 //
 // Weights and activations go through LDS by direct loads, each wave's own stages, a
 // few steps of 128 k ahead: loads return in order, so one counted wait a step covers
-// them, and no wave waits for another.
+// them, and no wave waits for another.  Weights that are read once go past the
+// caches when there are many (one token 58 us instead of 64, 32 tokens 613 instead
+// of 664).
 #include "experts_internal.h"
 
 namespace ep {
@@ -58,6 +60,7 @@ struct Rows {
     __device__ __forceinline__ static int64_t bytes(int n) { return int64_t(16) * n * (FP8 ? 1 : 2); }
     __device__ __forceinline__ static int swizzle(int r) { return FP8 ? (r >> 1) & 7 : r & 15; }
     // r: the 16 rows of n values; zeros from k value n on
+    template <bool NT>
     __device__ __forceinline__ static void load(__amdgpu_buffer_rsrc_t r, uint8_t* to, int step,
                                                 int n, int width, int lane) {
         constexpr int kChunks = kRow / 16;
@@ -65,9 +68,9 @@ struct Rows {
         for (int i = 0; i < kLoads; ++i) {
             const int row = i * kPerLoad + lane / kChunks;
             const int k = step * kStep + ((lane % kChunks) ^ swizzle(row)) * (FP8 ? 16 : 8);
-            load16_to_lds(r, to + i * 1024,
-                          k < n ? (uint32_t(row) * uint32_t(width) + uint32_t(k)) * (FP8 ? 1u : 2u)
-                                : kOutside);
+            load16_to_lds<NT>(r, to + i * 1024,
+                                  k < n ? (uint32_t(row) * uint32_t(width) + uint32_t(k)) * (FP8 ? 1u : 2u)
+                                    : kOutside);
         }
     }
     // Operands of the four matrix instructions of a step, times the block's scale:
@@ -145,7 +148,7 @@ struct Columns {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int k = step * kStep + chunk[i] * 8;
-            load16_to_lds(r, to + i * 1024, k < n ? at[i] + uint32_t(k) * 2u : kOutside);
+            load16_to_lds<false>(r, to + i * 1024, k < n ? at[i] + uint32_t(k) * 2u : kOutside);
         }
     }
     // operand i (of 4) of column tile t: the lane's column l (fewer than 16: again
@@ -189,7 +192,7 @@ constexpr int up_bytes() {
 }
 
 // Columns first .. first + C - 1 of the unit's m tokens.
-template <bool FP8, int C, int BYTES>
+template <bool FP8, int C, bool NT, int BYTES>
 __device__ __forceinline__ void up_body(const MoeArgs& p, int e, int n0, int m, int first_col,
                                         const uint8_t* token_of, const float* weight_of,
                                         const int* pick_of, uint8_t* lds)
@@ -227,8 +230,8 @@ __device__ __forceinline__ void up_body(const MoeArgs& p, int e, int n0, int m, 
     auto load = [&](int s, int a) {
         const int n = s < last ? H : 0;
         uint8_t* const to = stages + a * kStage;
-        W::load(gr, to, s, n, H, lane);
-        W::load(ur, to + W::kBytes, s, n, H, lane);
+        W::template load<NT>(gr, to, s, n, H, lane);
+        W::template load<NT>(ur, to + W::kBytes, s, n, H, lane);
         x.load(xr, to + 2 * W::kBytes, s, n);
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -319,7 +322,7 @@ __device__ __forceinline__ int only_pick(const MoeArgs& p, int u, int& mine, uin
 }
 
 // FEW: at most four tokens.
-template <bool FP8, bool FEW>
+template <bool FP8, bool FEW, bool NT>
 __global__ __launch_bounds__(kUpWaves* kWave) void moe_up_kernel(MoeArgs p)
 {
     // One array for all: with several, the compiler tells them apart and waits for
@@ -354,7 +357,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void moe_up_kernel(MoeArgs p)
             pick_of[0] = u;
         }
         __builtin_amdgcn_wave_barrier();
-        up_body<FP8, 4, kBytes>(p, e, chunk * 16, 1, 0, token_of, weight_of, pick_of, lds);
+        up_body<FP8, 4, NT, kBytes>(p, e, chunk * 16, 1, 0, token_of, weight_of, pick_of, lds);
         return;
     }
 
@@ -430,13 +433,13 @@ __global__ __launch_bounds__(kUpWaves* kWave) void moe_up_kernel(MoeArgs p)
     }
     __builtin_amdgcn_wave_barrier();
     if (m <= 4) {
-        up_body<FP8, 4, kBytes>(p, e, n0, m, 0, token_of, weight_of, pick_of, lds);
+        up_body<FP8, 4, NT, kBytes>(p, e, n0, m, 0, token_of, weight_of, pick_of, lds);
     } else if constexpr (!FEW) {
         if (m <= 16) {
-            up_body<FP8, 16, kBytes>(p, e, n0, m, 0, token_of, weight_of, pick_of, lds);
+            up_body<FP8, 16, NT, kBytes>(p, e, n0, m, 0, token_of, weight_of, pick_of, lds);
         } else {
             for (int c = 0; c < m; c += 32)
-                up_body<FP8, 32, kBytes>(p, e, n0, m, c, token_of, weight_of, pick_of, lds);
+                up_body<FP8, 32, false, kBytes>(p, e, n0, m, c, token_of, weight_of, pick_of, lds);
         }
     }
 }
@@ -445,7 +448,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void moe_up_kernel(MoeArgs p)
 // A wave's expert, tokens first .. first + C / 2 - 1 of its m, into
 // sums[token][16].  The C columns are the tokens' high halves, then their low ones;
 // a token's two columns are added at the end.  With one token its pick is `only`.
-template <bool FP8, int C, int STAGES>
+template <bool FP8, int C, bool NT, int STAGES>
 __device__ __forceinline__ void down_body(const MoeArgs& p, int e, int n0, int m, int first,
                                           int only, const int32_t* picks, uint8_t* stage,
                                           f32x4* sums)
@@ -474,7 +477,7 @@ __device__ __forceinline__ void down_body(const MoeArgs& p, int e, int n0, int m
     }
     auto load = [&](int s, int a) {
         const int n = s < steps ? I : 0;
-        W::load(wr, stage + a * kStage, s, n, I, lane);
+        W::template load<NT>(wr, stage + a * kStage, s, n, I, lane);
         x.load(hr, stage + a * kStage + W::kBytes, s, n);
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -530,7 +533,7 @@ constexpr int down_bytes() {
 }
 
 // TMAX tokens at most.
-template <bool FP8, int TMAX, int WAVES>
+template <bool FP8, int TMAX, int WAVES, bool NT>
 __global__ __launch_bounds__(WAVES* kWave) void moe_down_kernel(MoeArgs p)
 {
     constexpr int kSums = TMAX * 4, kDownBytes = down_bytes<FP8, TMAX>();      // a wave's
@@ -551,16 +554,16 @@ __global__ __launch_bounds__(WAVES* kWave) void moe_down_kernel(MoeArgs p)
             uint64_t same;
             const int e = only_pick(p, u, mine, same);
             if (e >= 0)
-                down_body<FP8, 4, down_stages(FP8, 4)>(p, e, n0, 1, 0, u, nullptr, stage, to);
+                down_body<FP8, 4, NT, down_stages(FP8, 4)>(p, e, n0, 1, 0, u, nullptr, stage, to);
         } else {
             const int32_t* unit = p.units + kHead + int64_t(u) * kUnit;
             const int e = unit[0], m = unit[1], only = unit[2];
             if (m <= 4) {
-                down_body<FP8, 8, down_stages(FP8, 8)>(p, e, n0, m, 0, only, unit + 2, stage, to);
+                down_body<FP8, 8, NT, down_stages(FP8, 8)>(p, e, n0, m, 0, only, unit + 2, stage, to);
             } else {
                 for (int c = 0; c < m; c += 8)
-                    down_body<FP8, 16, down_stages(FP8, 16)>(p, e, n0, m, c, only, unit + 2, stage,
-                                                             to);
+                    down_body<FP8, 16, false, down_stages(FP8, 16)>(p, e, n0, m, c, only,
+                                                                    unit + 2, stage, to);
             }
         }
     }
@@ -576,20 +579,23 @@ __global__ __launch_bounds__(WAVES* kWave) void moe_down_kernel(MoeArgs p)
     }
 }
 
-template <bool FP8>
+template <bool FP8, bool NT>
 hipError_t launch(const MoeArgs& p, hipStream_t s)
 {
     const int picks = p.T * p.k;
     const dim3 up(uint32_t(p.I / 16), uint32_t(picks < p.E ? picks : p.E)), block(kUpWaves * kWave);
-    if (p.T <= 4) EP_LAUNCH((moe_up_kernel<FP8, true>), up, block, 0, s, p);
-    else EP_LAUNCH((moe_up_kernel<FP8, false>), up, block, 0, s, p);
+    if (p.T <= 4) EP_LAUNCH((moe_up_kernel<FP8, true, NT>), up, block, 0, s, p);
+    else EP_LAUNCH((moe_up_kernel<FP8, false, NT>), up, block, 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // sums in LDS for as few tokens as will do: more workgroups a CU
     const dim3 down(uint32_t(p.H / 16));
-    if (p.T == 1) EP_LAUNCH((moe_down_kernel<FP8, 1, 8>), down, dim3(8 * kWave), 0, s, p);
-    else if (p.T <= 32) EP_LAUNCH((moe_down_kernel<FP8, 32, 4>), down, dim3(4 * kWave), 0, s, p);
-    else EP_LAUNCH((moe_down_kernel<FP8, kMoeMaxTokens, 4>), down, dim3(4 * kWave), 0, s, p);
+    if (p.T == 1)
+        EP_LAUNCH((moe_down_kernel<FP8, 1, 8, NT>), down, dim3(8 * kWave), 0, s, p);
+    else if (p.T <= 32)
+        EP_LAUNCH((moe_down_kernel<FP8, 32, 4, NT>), down, dim3(4 * kWave), 0, s, p);
+    else
+        EP_LAUNCH((moe_down_kernel<FP8, kMoeMaxTokens, 4, NT>), down, dim3(4 * kWave), 0, s, p);
     return hipGetLastError();
 }
 
@@ -613,7 +619,9 @@ hipError_t launch_moe_tokens(const uint16_t* x, const int32_t* idx, const float*
                     static_cast<const uint8_t*>(w2), w2_scale, out,
                     reinterpret_cast<uint16_t*>(base),
                     reinterpret_cast<int32_t*>(base + h_bytes)};
-    return w13_scale ? launch<true>(p, s) : launch<false>(p, s);
+    const bool large = int64_t(E) * 3 * I * H * (w13_scale ? 1 : 2) > kStreamBytes;
+    if (w13_scale) return large ? launch<true, true>(p, s) : launch<true, false>(p, s);
+    return large ? launch<false, true>(p, s) : launch<false, false>(p, s);
 }
 
 }  // namespace ep

@@ -149,6 +149,8 @@ SHAPES = [
     ([70] * 69 + [0], 0, 3, 1040, 272),
     ([11] * 15 + [100], 0, 0, 2816, 400),
     ([40, 0, 9], 0, 2, 272, 8464),
+    ([11] * 15 + [100], 0, 0, 2816, 1664), ([9] * 8, 2, 0, 4096, 2064),     # weights over 64 MB
+    ([4] * 64, 0, 1, 1040, 1040), ([20], 0, 0, 4096, 16640),
     ([70, 20, 60, 0, 50, 90, 49, 61, 60], 1, 0, 4112, 8320),
 ]
 
@@ -246,7 +248,7 @@ def test_expert_offsets_out_of_order(ep, bad):
     ([1], 0, 0, 128, 16), ([0, 3, 20, 0], 1, 2, 256, 208), ([40, 0, 65], 0, 3, 384, 336),
     ([300, 5, 0, 600], 2, 1, 256, 1040), ([1500], 0, 0, 1408, 512),
     ([2000, 0, 1500, 700], 0, 5, 2816, 400), ([70] * 66, 0, 0, 512, 144),
-    ([20, 3], 0, 1, 128, 8336), ([90] * 10, 0, 0, 1792, 8208)])
+    ([20, 3], 0, 1, 128, 8336), ([90] * 10, 0, 0, 1792, 8208), ([30] * 10, 0, 0, 1792, 2000)])
 def test_expert_swiglu(ep, counts, before, behind, I, K, save):
     E, S = len(counts), sum(counts) + before + behind
     say(f"expert swiglu E={E} S={S} I={I} K={K} save={save}")
@@ -429,7 +431,8 @@ MOE = [(1, 16, 128, 1, 1, True), (1, 7168, 256, 16, 8, True), (3, 208, 128, 8, 2
        (1, 16, 16, 1, 1, False), (2, 4096, 1408, 9, 8, False), (5, 144, 80, 6, 2, False),
        (2, 8336, 128, 3, 2, True), (2, 256, 8320, 3, 2, True), (1, 8336, 8320, 2, 2, True),
        (48, 144, 128, 1, 1, True), (9, 528, 128, 20, 12, True), (5, 1040, 256, 3, 3, True),
-       (40, 144, 80, 1, 1, False), (1, 272, 80, 20, 16, False), (3, 8336, 48, 2, 2, False),
+       (8, 4096, 512, 12, 4, True), (40, 4096, 256, 12, 2, False),          # weights over 64 MB
+       (64, 4096, 256, 24, 2, True), (40, 144, 80, 1, 1, False), (1, 272, 80, 20, 16, False), (3, 8336, 48, 2, 2, False),
        (31, 336, 48, 4, 3, False), (64, 256, 112, 2, 1, False), (64, 128, 64, 64, 64, False)]
 
 
