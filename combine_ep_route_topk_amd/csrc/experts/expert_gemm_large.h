@@ -17,16 +17,17 @@
 // tiles, so that the first loads of a tile and the stores of the one before it
 // hide behind matrix work.
 //
-// Measured on MI355X, 8 experts: 32768 rows x 7168 x 4096 in 785 us, 32768 x
-// 4096 x 7168 in 753 us (2.45, 2.56 PFLOP/s; a library product of one matrix of
-// that size 683 and 593 us).  The steps before, at the first size: eight waves of
-// 128 x 64 on two stages 1062; four waves, 64 bytes of k on four stages, all
-// loads of a step at once 990 (rows of 64 bytes ask the L2 for half lines); whole
-// lines on two stages with one load after each matrix instruction 954 (all at once
-// 964: the wave stalls behind its own loads); five stages 865; persistent 785.
-// What bounds it now: power (the clock falls to about 1.9 GHz; register-only matrix
-// work on random data reaches 3.8 PFLOP/s) and the loads' way from L2 into LDS,
-// about 23 bytes a cycle and CU when they hit.
+// Measured on MI355X, 8 experts, sustained: 32768 rows x 7168 x 4096 in 802 to 820
+// us, 32768 x 4096 x 7168 in 765 to 811 (2.35 to 2.5 PFLOP/s; a library product of
+// one matrix of that size 656 to 692 and 611), the same gated 744.  The steps
+// before, at the first size: eight waves of 128 x 64 on two stages 1062; four
+// waves, 64 bytes of k on four stages, all loads of a step at once 990 (rows of 64
+// bytes ask the L2 for half lines); whole lines on two stages with one load after
+// each matrix instruction 954 (all at once 964: the wave stalls behind its own
+// loads); five stages 865; persistent 830; whole-line stores 815.  What bounds it
+// now: power (the clock falls to about 1.9 GHz; register-only matrix work on random
+// data reaches 3.8 PFLOP/s), and that loads and stores complete in order: a tile's
+// third step waits for the last tile's stores.
 #pragma once
 
 #include "experts_internal.h"
@@ -128,7 +129,6 @@ __device__ __forceinline__ void hide(int& v) {
     asm volatile("" : "+v"(v));
 #endif
 }
-
 
 constexpr int kLargeTile = 256;
 
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(256, 1) void expert_gemm_large_kernel(GemmArgs p)
         uint8_t* const scratch = lds + (wslot == 0 ? 2 : wslot - 1) * kStage;
         if constexpr (!GATED) {
             // 32 tokens x 128 weight rows at a time through 8 KB of the wave's own,
-            // so that stores write whole lines, past the caches, where tokens and
-            // weights are read again (32-byte parts of lines, straight from
+            // so that stores write whole lines, and past the caches, where tokens
+            // and weights are read again (32-byte parts of lines straight from
             // registers: 32768 rows x 7168 x 4096 830 us, so 815): rows of 256
             // bytes, chunk c of 16 of row r at c ^ r % 16
             uint8_t* const mine = scratch + wave * 8192;

@@ -5,7 +5,9 @@
 // max|x| / s <= 448 over the block.  Reading is one pass: a block's 128 values
 // sit in 8 lanes of one wave, its maximum takes three lane exchanges, and the
 // quantised values go straight to the rows' final places -- for ep_dispatch_fp8
-// to each of the token's k rows of the expert-contiguous buffer.
+// to each of the token's k rows of the expert-contiguous buffer.  HBM-bound, most
+// of it writes: 4096 tokens of 7168 to 8 rows each in 48 us on MI355X, 6.1 TB/s; 64
+// tokens in 4 us, one round of latency.
 #include "experts_internal.h"
 
 namespace ep {
