@@ -576,6 +576,19 @@ def _launch(fn, dev, stream, tensors, *args) -> None:
             _check(fn(*args, _stream(stream, dev)))
 
 
+def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
+    """A workspace that only this call knows, from the memory of the stream that the call runs on:
+    the allocator hands it out again, once it is dropped, in that stream's order."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream, dev)
+        stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
+                  else torch.cuda.default_stream(dev))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
 def ep_quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None,
                     scale: torch.Tensor | None = None, stream=None):
     """x bf16 [S][H] -> (q e4m3 [S][H], scale u8 [S][ceil(H/128)])."""
@@ -747,7 +760,7 @@ def ep_expert_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     if workspace is None:
         need = ep_expert_wgrad_workspace_bytes(S, N, K, E)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _scratch(need, dev, stream)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
     _launch(_lib.ep_expert_wgrad, dev, stream, (x, expert_offsets, grad_w, workspace),
@@ -790,8 +803,7 @@ def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     if out is None:
         out = torch.empty((T, H), dtype=x.dtype, device=dev)
     if workspace is None:
-        workspace = torch.empty(ep_moe_tokens_workspace_bytes(T, k, I), dtype=torch.uint8,
-                                device=dev)
+        workspace = _scratch(ep_moe_tokens_workspace_bytes(T, k, I), dev, stream)
     _bits_ok(out, "out", (T, H))
     _need(workspace, "workspace", torch.uint8)
     _launch(_lib.ep_moe_tokens, dev, stream,

@@ -665,6 +665,46 @@ def test_two_streams(ep):
             assert torch.equal(o, want[i])
 
 
+@pytest.mark.parametrize("handle", ["stream", "integer", "null"])
+def test_own_workspace_belongs_to_the_calls_stream(ep, handle, monkeypatch):
+    """A workspace made inside a call on another stream is not handed out on the current one while
+    the call may still run."""
+    s = torch.cuda.Stream()
+    stream = {"stream": s, "integer": s.cuda_stream, "null": 0}[handle]
+    c = moe_case(ep, 24, 512, 256, 8, 4, True)
+    want = ep.ep_moe_tokens(**c)
+    g = gen(2)
+    dy, x, off = normal(g, 4096, 256), normal(g, 4096, 256), offsets_of([4096])
+    dw = ep.ep_expert_wgrad(dy, x, off)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    used = []
+
+    def spy(name, at):
+        real = getattr(ep.library(), name)
+
+        def call(*args):
+            used.append(args[at])
+            return real(*args)
+        monkeypatch.setattr(ep.library(), name, call)
+
+    spy("ep_moe_tokens", 13)
+    spy("ep_expert_wgrad", 9)
+    say(f"own workspace on {handle}")
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.current_stream().synchronize()
+        out = ep.ep_moe_tokens(**c, stream=stream)
+        n = ep.ep_moe_tokens_workspace_bytes(24, 4, 256)
+        mine = torch.empty(n, dtype=torch.uint8, device=DEV)
+        dw2 = ep.ep_expert_wgrad(dy, x, off, stream=stream)
+        m = ep.ep_expert_wgrad_workspace_bytes(4096, 256, 256, 1)
+        mine2 = torch.empty(m, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    assert m > 0 and all(used)
+    assert used[0] != mine.data_ptr() and used[1] != mine2.data_ptr()
+    assert torch.equal(out, want) and torch.equal(dw2, dw)
+
+
 def test_timing_events(ep):
     """The one-shot measurement hook brackets an expert operator's kernels."""
     ev = ep.HipEvents()
