@@ -386,6 +386,47 @@ def test_no_rows(ep):
     assert (dw == 0).all()
 
 
+def test_offsets_past_32_bits(ep):
+    """2.3e9 values in a buffer: rows on both sides of 2^31 values and bytes, and sums over all."""
+    g = gen(21)
+    S, K, N = 1_130_000, 2048, 128
+    say(f"offsets past 32 bits S={S} K={K}")
+    x = torch.empty((S, K), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    q, sc = ep.ep_quantize_fp8(x)
+    w, w_s = weights_of(ep, g, 2, N, K)
+    cut = 2 ** 31 // K - 5                             # the second segment straddles 2^31 bytes
+    off = torch.tensor([0, cut, S], dtype=torch.int32, device=DEV)
+    y = ep.ep_expert_gemm_fp8(q, sc, w, w_s, off)
+    torch.cuda.synchronize()
+    rows = torch.cat([torch.arange(lo, lo + 20) for lo in (0, cut - 10, 2 ** 31 // K - 10, S - 20)])
+    rows = rows.to(DEV)
+    wantq, byte = ref.quantize_rows(x[rows])
+    assert torch.equal(sc[rows], byte)
+    same_e4m3(q.view(torch.uint8)[rows].view(torch.float8_e4m3fn), wantq, "q")
+    a = ref.values(q.view(torch.uint8)[rows].view(torch.float8_e4m3fn), sc[rows])
+    wv = ref.weight_values(w, w_s)[(rows >= cut).long()]
+    want, mag = (wv @ a[:, :, None])[..., 0], (wv.abs() @ a.abs()[:, :, None])[..., 0]
+    close(y[rows], want, BF16 * want.abs() + ref.sum_bound(K, mag), "y")
+    del q, sc
+
+    dw = ep.ep_expert_wgrad(y, x, off)
+    torch.cuda.synchronize()
+    want = torch.zeros(2, N, K, dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(want)
+    for e, lo, hi in ref.segments(off):
+        for b in range(lo, hi, 1 << 17):
+            yy, xx = y[b:min(b + (1 << 17), hi)].double(), x[b:min(b + (1 << 17), hi)].double()
+            want[e] += yy.t() @ xx
+            mag[e] += yy.abs().t() @ xx.abs()
+    close(dw, want, ref.sum_bound(S, mag) + F32 * want.abs(), "dw")
+
+    dh = torch.empty((S, K // 2), dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    dgu, h = ep.ep_swiglu_grad(dh, x)                  # x as the saved gate and up values
+    some = ep.ep_swiglu_grad(dh[rows].contiguous(), x[rows].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(dgu[rows], some[0]) and torch.equal(h[rows], some[1])
+
+
 # ----------------------------------------------------------------- few tokens
 def moe_case(ep, T, H, I, E, k, fp8, seed=0):
     g = gen(T * 1000 + H + I + seed)
