@@ -3,11 +3,13 @@
 //   h[t][j] = w[t][j] silu(G) * U,  [G; U] = W13[e] x[t],  e = idx[t][j]
 //   out[t]  = sum_j W2[e] h[t][j]
 //
-// Bound by the bytes of the picked experts' weights: each is read once for up to
-// 32 (first launch) or 16 (second) tokens that picked it, 16 rows at a time as the
-// matrix instruction's row operand, with the tokens as its columns.  8-bit weights become bf16 times their block's power
-// of two on the way (exact); h is kept as two bf16 halves (16 bits of mantissa),
-// so that no step rounds to fewer bits than the products need.
+// Bound by the bytes of the picked experts' weights: each is read once for up to 32
+// (first launch) or 8 (second) tokens that picked it, 16 rows at a time as the
+// matrix instruction's row operand, with the tokens as its columns.  8-bit weights
+// become bf16 times their block's power of two on the way (exact for 2^-117 to
+// 2^119); h is kept as two bf16 halves (16 bits of mantissa), two columns of the
+// second launch's product, so that no step rounds to fewer bits than the products
+// need.
 //
 // First launch: one workgroup per (picked expert, 16 outputs of I), which finds
 // its expert from the picks alone.  Its waves split H and join in LDS.  Second

@@ -597,8 +597,10 @@ ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32
  * The whole layer for 1 <= T <= 64 tokens (one decoding step), in two launches:
  *   out[t] = sum_j topk_w[t][j] W2[e] (silu(g) * u), [g; u] = W13[e] x[t],
  *   e = topk_idx[t][j].
- * Activations are not quantised; sums are f32 and out is rounded once.  Each
- * picked expert's weights are read once, whatever the tokens that picked it.
+ * Activations are not quantised; sums are f32 and out is rounded once.  A
+ * picked expert's first weights are read once for up to 32 tokens that picked
+ * it, its second ones for up to 8.  8-bit weights become bf16 times their scale:
+ * exact for scale bytes from 10 to 246.
  * A pick outside [0, E) contributes nothing (a token without any gets zeros);
  * an expert picked twice by a token counts with both weights.  The result is
  * the same on every call.

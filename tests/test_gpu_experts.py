@@ -512,6 +512,20 @@ def test_moe_tokens_picks(ep, fp8):
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("T", [1, 12])
+@pytest.mark.parametrize("byte,weight", [(10, 1e34), (246, 1e-30)])
+def test_moe_tokens_scale_range(ep, T, byte, weight):
+    """The smallest and the largest scale that 8-bit weights are exact for."""
+    c = moe_case(ep, T, 256, 128, 3, 2, True)
+    c["w2_scale"].fill_(byte)
+    c["topk_w"] *= weight
+    say(f"moe tokens T={T} scale byte {byte}")
+    out = ep.ep_moe_tokens(**c)
+    torch.cuda.synchronize()
+    want, bound = moe_ref(c)
+    close(out, want, bound, "out")
+
+
 @pytest.mark.parametrize("fp8", [True, False])
 def test_moe_one_token_picks(ep, fp8):
     """One token: picks outside [0, E), an expert picked three times, no pick at all."""
