@@ -7,7 +7,9 @@
 // matrix core's registers: no multiply-add per block on the vector ALU.  The
 // weights are its row operand: a lane then holds four neighbouring n of one
 // token.  (The unit sums a block's 8-bit products to about 17 bits: results are
-// 1.6e-5 off the exact sum, for one block as for many.)
+// 1.6e-5 off the exact sum, for one block as for many; of h some 0.16% of the
+// values then round to their e4m3 neighbour.  Products of bf16, summed in f32, keep
+// them, but take 64 us instead of 52 gated, 8 experts x 4096 x 7168, 32 rows each.)
 //
 // Segments of many rows are bound by matrix work and take the kernel of
 // expert_gemm_large.h; the one here is for few rows, where the weights' bytes

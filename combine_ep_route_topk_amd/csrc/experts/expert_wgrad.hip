@@ -90,7 +90,7 @@ __device__ __forceinline__ void put_fragments(__amdgpu_buffer_rsrc_t r, uint8_t*
 // all waves meet: this step's stages have been read, the next step's have
 // landed.  The stream runs on across tiles.
 //
-// Measured on MI355X, 8 experts x 4096 x 7168, 4096 rows each: 1525 to 1550 us (1.25
+// Measured on MI355X, 8 experts x 4096 x 7168, 4096 rows each: 1507 to 1550 us (1.26
 // PFLOP/s; a library product of one matrix of that size with the same transposed
 // operands 1974 to 2035, with both turned beforehand 1530 to 1600); eight waves of 128 x 64 on two stages,
 // without the units' exchange, 3721 us, all of it LDS bank conflicts.
