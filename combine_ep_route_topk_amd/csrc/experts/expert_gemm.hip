@@ -30,7 +30,10 @@ template <int TM, int WAVES, int ROWS, bool GATED, bool NT>
 __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmArgs p)
 {
     constexpr int kDepth = 3, kBK = kScaleBlock, TN = ROWS * WAVES, NF = ROWS / 16;
-    constexpr int FM = TM / 16, kXLoads = TM / 8 / WAVES, kWStage = ROWS * kBK, kXStage = TM * kBK;
+    // every wave loads whole 1 KB pieces of the tokens (rows past TM are zeros)
+    constexpr int kXRows = TM > 8 * WAVES ? TM : 8 * WAVES;
+    constexpr int FM = TM / 16, kXLoads = kXRows / 8 / WAVES, kWStage = ROWS * kBK;
+    constexpr int kXStage = kXRows * kBK;
     static_assert(!GATED || (TN == 256 && ROWS == 32), "a gated tile makes one scale block");
     constexpr int kOps = ROWS / 8 + kXLoads;               // loads of one step
     constexpr int kPitch = 68;                      // 64 scale bytes of a token, padded
@@ -276,6 +279,10 @@ hipError_t launch_large(GemmArgs p, hipStream_t s)
 //   8 x 4096 x 7168, 32 rows                56 / 44 / 45
 //   2 x 4096 x 7168, 8 rows                 29 / 23 / 20
 //   32 x 4096 x 7168, 16 rows              161 / 160 / 165
+// With 256 weight rows (gated always), 64 / 32 tokens a workgroup, gated:
+//   8 x 4096 x 7168, 48 rows 55 / 50;  1 x 4096 x 7168, 64 rows 39 / 31;  4 x 1024 x
+//   2048, 300 rows 17 / 14;  16 x 2816 x 4096, 30 rows 34 / 33, 45 rows 35 / 53;
+//   32 x 4096 x 4096, 48 rows 94 / 130
 // One workgroup a CU has room for 128 rows: where the 32 rows are an average, of 94
 // to 12, 53 us instead of 64.
 template <bool GATED>
@@ -297,6 +304,9 @@ hipError_t launch(const GemmArgs& p, hipStream_t s)
             return launch_stream<64, 4, 32, false>(p, s);
         }
     }
+    // a last, partly filled tile for every other expert
+    const int64_t few = (int64_t(p.S) / 32 + p.E / 2) * ((p.N + 255) / 256);
+    if (few <= cus) return launch_stream<32, 8, 32, GATED>(p, s);
     return launch_stream<64, 8, 32, GATED>(p, s);
 }
 

@@ -150,7 +150,7 @@ SHAPES = [
     ([11] * 15 + [100], 0, 0, 2816, 400),
     ([40, 0, 9], 0, 2, 272, 8464),
     ([11] * 15 + [100], 0, 0, 2816, 1664), ([9] * 8, 2, 0, 4096, 2064),     # weights over 64 MB
-    ([4] * 64, 0, 1, 1040, 1040), ([20], 0, 0, 4096, 16640),
+    ([45] * 18, 0, 1, 2816, 144), ([45] * 18, 0, 0, 2816, 1440), ([4] * 64, 0, 1, 1040, 1040), ([20], 0, 0, 4096, 16640),
     ([70, 20, 60, 0, 50, 90, 49, 61, 60], 1, 0, 4112, 8320),
 ]
 
@@ -248,7 +248,8 @@ def test_expert_offsets_out_of_order(ep, bad):
     ([1], 0, 0, 128, 16), ([0, 3, 20, 0], 1, 2, 256, 208), ([40, 0, 65], 0, 3, 384, 336),
     ([300, 5, 0, 600], 2, 1, 256, 1040), ([1500], 0, 0, 1408, 512),
     ([2000, 0, 1500, 700], 0, 5, 2816, 400), ([70] * 66, 0, 0, 512, 144),
-    ([20, 3], 0, 1, 128, 8336), ([90] * 10, 0, 0, 1792, 8208), ([30] * 10, 0, 0, 1792, 2000)])
+    ([20, 3], 0, 1, 128, 8336), ([90] * 10, 0, 0, 1792, 8208), ([30] * 10, 0, 0, 1792, 2000),
+    ([45] * 18, 3, 0, 1792, 208), ([45] * 18, 0, 1, 1792, 2000)])
 def test_expert_swiglu(ep, counts, before, behind, I, K, save):
     E, S = len(counts), sum(counts) + before + behind
     say(f"expert swiglu E={E} S={S} I={I} K={K} save={save}")
