@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kUpWaves = 4;       // first launch: waves that split H
 constexpr int kStep = 128;        // k values per step: 32 of one row in each lane
+constexpr float kBf16Max = 0x1.fep127f;
 
 struct MoeArgs {
     const uint16_t* x;
@@ -300,8 +301,12 @@ __device__ __forceinline__ void up_body(const MoeArgs& p, int e, int n0, int m, 
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const float h = w * (vg[c] * sigmoid(vg[c]) * vu[c]);
+            // h that rounds past bf16's largest value keeps that as its high half and
+            // the rest as its low one; an infinite h has no rest (inf - inf is NaN).
+            const bool finite = fabsf(h) < __builtin_inff();
             hi[c] = bf16_lo(pack_bf16x2(h, 0.0f));
-            lo[c] = h - hi[c];
+            if (finite) hi[c] = fminf(fmaxf(hi[c], -kBf16Max), kBf16Max);
+            lo[c] = finite ? h - hi[c] : 0.0f;
         }
         const int64_t at = int64_t(pick_of[col]) * I + n0 + g * 4;
         *reinterpret_cast<u32x2*>(p.h + at) =

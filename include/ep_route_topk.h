@@ -597,8 +597,10 @@ ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32
  * The whole layer for 1 <= T <= 64 tokens (one decoding step), in two launches:
  *   out[t] = sum_j topk_w[t][j] W2[e] (silu(g) * u), [g; u] = W13[e] x[t],
  *   e = topk_idx[t][j].
- * Activations are not quantised; sums are f32 and out is rounded once.  A
- * picked expert's first weights are read once for up to 32 tokens that picked
+ * Activations are not quantised; sums are f32 and out is rounded once.  topk_w
+ * joins silu(g) * u in f32 before the second product, which takes the result as
+ * two bf16 halves: 16 bits of mantissa over f32's whole range; an infinity stays
+ * one.  A picked expert's first weights are read once for up to 32 tokens that picked
  * it, its second ones for up to 8.  8-bit weights become bf16 times their scale:
  * exact for scale bytes from 10 to 246.
  * A pick outside [0, E) contributes nothing (a token without any gets zeros);
