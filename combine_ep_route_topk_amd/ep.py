@@ -6,6 +6,13 @@ streams); bf16 tensors are passed as their raw 16-bit patterns.  Functions
 mirror the C entry points of the same name; outputs may be passed in
 pre-allocated (the benchmark does) or are allocated here with torch.empty.
 
+`stream` (a torch stream or a raw handle; default: the current one) is the
+stream that a call's kernels run on.  As in a `with torch.cuda.stream(stream)`
+block, what an expert operator allocates belongs to that stream, and the caller
+orders the rest: tensors passed in are ready on it, and they, like results used
+on other streams, are not dropped before the work that uses them is done
+(Tensor.record_stream, or a wait).
+
 Importing this module loads the built library and fails loudly if it is
 missing: there is no CPU fallback.
 """
@@ -121,6 +128,25 @@ def _stream(stream, device) -> int:
     if stream is None:        # the handle alone: a Stream object takes 2 us to make
         return _current_stream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_object(stream, dev) -> torch.cuda.Stream:
+    """The torch stream of a stream argument (a torch stream or a raw handle)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream, dev)
+    return (torch.cuda.ExternalStream(handle, device=dev) if handle
+            else torch.cuda.default_stream(dev))
+
+
+def _empty(shape, dtype: torch.dtype, dev, stream) -> torch.Tensor:
+    """An output or a workspace made inside a call, from the memory of the stream that the call runs
+    on.  From another stream's, the block may be one that work pending there still uses, and the
+    allocator would hand it out there again, once it is dropped, while the call still runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(_stream_object(stream, dev)):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -576,19 +602,6 @@ def _launch(fn, dev, stream, tensors, *args) -> None:
             _check(fn(*args, _stream(stream, dev)))
 
 
-def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
-    """A workspace that only this call knows, from the memory of the stream that the call runs on:
-    the allocator hands it out again, once it is dropped, in that stream's order."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream, dev)
-        stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
-                  else torch.cuda.default_stream(dev))
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-
-
 def ep_quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None,
                     scale: torch.Tensor | None = None, stream=None):
     """x bf16 [S][H] -> (q e4m3 [S][H], scale u8 [S][ceil(H/128)])."""
@@ -596,11 +609,11 @@ def ep_quantize_fp8(x: torch.Tensor, q: torch.Tensor | None = None,
     _bits_ok(x, "x")
     dev, nb = x.device, scale_blocks(H)
     if q is None:
-        q = torch.empty((S, H), dtype=torch.float8_e4m3fn, device=dev)
+        q = _empty((S, H), torch.float8_e4m3fn, dev, stream)
     else:
         _need_one_of(q, "q", _FP8, (S, H))
     if scale is None:
-        scale = torch.empty((S, nb), dtype=torch.uint8, device=dev)
+        scale = _empty((S, nb), torch.uint8, dev, stream)
     else:
         _need_one_of(scale, "scale", _SCALE, (S, nb))
     _launch(_lib.ep_quantize_fp8, dev, stream, (q, scale), _ptr(x), S, H, _ptr(q), _ptr(scale))
@@ -616,11 +629,11 @@ def ep_dispatch_fp8(x: torch.Tensor, pos: torch.Tensor, send: torch.Tensor | Non
     _need(pos, "pos", torch.int32, (T, k))
     dev, nb = x.device, scale_blocks(H)
     if send is None:
-        send = torch.empty((T * k, H), dtype=torch.float8_e4m3fn, device=dev)
+        send = _empty((T * k, H), torch.float8_e4m3fn, dev, stream)
     else:
         _need_one_of(send, "send", _FP8, (T * k, H))
     if scale is None:
-        scale = torch.empty((T * k, nb), dtype=torch.uint8, device=dev)
+        scale = _empty((T * k, nb), torch.uint8, dev, stream)
     else:
         _need_one_of(scale, "scale", _SCALE, (T * k, nb))
     _launch(_lib.ep_dispatch_fp8, dev, stream, (pos, send, scale), _ptr(x), T, H, k, _ptr(pos),
@@ -636,11 +649,10 @@ def ep_quantize_weight_fp8(w: torch.Tensor, transposed: bool = False, out: dict 
     _bits_ok(w, "w")
     dev, nb, kb = w.device, scale_blocks(N), scale_blocks(K)
     if out is None:
-        f8 = dict(dtype=torch.float8_e4m3fn, device=dev)
-        u8 = dict(dtype=torch.uint8, device=dev)
-        out = dict(q=torch.empty((E, N, K), **f8), scale=torch.empty((E, nb, kb), **u8))
+        f8, u8 = (torch.float8_e4m3fn, dev, stream), (torch.uint8, dev, stream)
+        out = dict(q=_empty((E, N, K), *f8), scale=_empty((E, nb, kb), *u8))
         if transposed:
-            out |= dict(q_t=torch.empty((E, K, N), **f8), scale_t=torch.empty((E, kb, nb), **u8))
+            out |= dict(q_t=_empty((E, K, N), *f8), scale_t=_empty((E, kb, nb), *u8))
     _need_one_of(out["q"], "q", _FP8, (E, N, K))
     _need_one_of(out["scale"], "scale", _SCALE, (E, nb, kb))
     q_t = scale_t = None
@@ -672,7 +684,7 @@ def ep_expert_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
     S, N, K, E = _expert_operands(a, a_scale, w, w_scale, expert_offsets, "w")
     dev = a.device
     if y is None:
-        y = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
+        y = _empty((S, N), torch.bfloat16, dev, stream)
     else:
         _bits_ok(y, "y", (S, N))
     _launch(_lib.ep_expert_gemm_fp8, dev, stream, (a_scale, w, w_scale, expert_offsets, y),
@@ -694,15 +706,15 @@ def ep_expert_swiglu_fp8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tens
         raise ValueError("w13 must hold as many gate rows as up rows")
     dev, I = a.device, N // 2
     if h is None:
-        h = torch.empty((S, I), dtype=torch.float8_e4m3fn, device=dev)
+        h = _empty((S, I), torch.float8_e4m3fn, dev, stream)
     else:
         _need_one_of(h, "h", _FP8, (S, I))
     if h_scale is None:
-        h_scale = torch.empty((S, scale_blocks(I)), dtype=torch.uint8, device=dev)
+        h_scale = _empty((S, scale_blocks(I)), torch.uint8, dev, stream)
     else:
         _need_one_of(h_scale, "h_scale", _SCALE, (S, scale_blocks(I)))
     if gate_up is None and save_gate_up:
-        gate_up = torch.empty((S, N), dtype=torch.bfloat16, device=dev)
+        gate_up = _empty((S, N), torch.bfloat16, dev, stream)
     if gate_up is not None:
         _bits_ok(gate_up, "gate_up", (S, N))
     _launch(_lib.ep_expert_swiglu_fp8, dev, stream,
@@ -721,11 +733,11 @@ def ep_swiglu_grad(grad_h: torch.Tensor, gate_up: torch.Tensor,
     _bits_ok(gate_up, "gate_up", (S, 2 * I))
     dev = grad_h.device
     if grad_gate_up is None:
-        grad_gate_up = torch.empty((S, 2 * I), dtype=gate_up.dtype, device=dev)
+        grad_gate_up = _empty((S, 2 * I), gate_up.dtype, dev, stream)
     else:
         _bits_ok(grad_gate_up, "grad_gate_up", (S, 2 * I))
     if h is None:
-        h = torch.empty((S, I), dtype=grad_h.dtype, device=dev)
+        h = _empty((S, I), grad_h.dtype, dev, stream)
     else:
         _bits_ok(h, "h", (S, I))
     _launch(_lib.ep_swiglu_grad, dev, stream, (gate_up, grad_gate_up, h), _ptr(grad_h),
@@ -755,12 +767,12 @@ def ep_expert_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     if grad_w is None:
         if accumulate:
             raise ValueError("accumulate needs the grad_w to add to")
-        grad_w = torch.empty((E, N, K), dtype=torch.float32, device=dev)
+        grad_w = _empty((E, N, K), torch.float32, dev, stream)
     _need(grad_w, "grad_w", torch.float32, (E, N, K))
     if workspace is None:
         need = ep_expert_wgrad_workspace_bytes(S, N, K, E)
         if need:
-            workspace = _scratch(need, dev, stream)
+            workspace = _empty(need, torch.uint8, dev, stream)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
     _launch(_lib.ep_expert_wgrad, dev, stream, (x, expert_offsets, grad_w, workspace),
@@ -801,9 +813,9 @@ def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
         _need_one_of(w2_scale, "w2_scale", _SCALE, (E, scale_blocks(H), scale_blocks(I)))
     dev = x.device
     if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=dev)
+        out = _empty((T, H), x.dtype, dev, stream)
     if workspace is None:
-        workspace = _scratch(ep_moe_tokens_workspace_bytes(T, k, I), dev, stream)
+        workspace = _empty(ep_moe_tokens_workspace_bytes(T, k, I), torch.uint8, dev, stream)
     _bits_ok(out, "out", (T, H))
     _need(workspace, "workspace", torch.uint8)
     _launch(_lib.ep_moe_tokens, dev, stream,

@@ -1,0 +1,121 @@
+"""stream=: what a call makes for itself belongs to the stream that its kernels run on, so that neither
+work pending on the current stream nor a later owner of the memory meets the call."""
+import pytest
+import torch
+
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ep():
+    from combine_ep_route_topk_amd import ep as mod
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    return mod
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def normal(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV).to(torch.bfloat16)
+
+
+def pool_of(t):
+    """The raw handle of the stream whose memory holds the tensor."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def tensors(v):
+    if isinstance(v, torch.Tensor):
+        return [v]
+    if isinstance(v, dict):
+        v = list(v.values())
+    return [t for x in v for t in tensors(x)] if isinstance(v, (list, tuple)) else []
+
+
+def calls(ep):
+    """name -> (a call with stream=, whose outputs are all its own): small inputs of every operator."""
+    g = gen(7)
+    T, H, I, E, k = 24, 256, 128, 4, 2
+    x, logits = normal(g, T, H), torch.randn((T, E), generator=g, device=DEV)
+    idx, tw = ep.ep_route_topk(logits, k)
+    lay = ep.ep_dispatch_layout(idx, E, 2)
+    pos, off = lay["pos"], lay["expert_offsets"]
+    w13, w2 = normal(g, E, 2 * I, H), normal(g, E, H, I)
+    d13, d2 = ep.ep_quantize_weight_fp8(w13), ep.ep_quantize_weight_fp8(w2)
+    a, a_s = ep.ep_dispatch_fp8(x, pos)
+    gu, dh = normal(g, T * k, 2 * I), normal(g, T * k, I)
+    rows = normal(g, 4096, 256)
+    one = torch.tensor([0, 4096], dtype=torch.int32, device=DEV)
+    return {
+        "quantize": lambda s: ep.ep_quantize_fp8(x, stream=s),
+        "dispatch_fp8": lambda s: ep.ep_dispatch_fp8(x, pos, stream=s),
+        "quantize_weight": lambda s: ep.ep_quantize_weight_fp8(w13, transposed=True, stream=s),
+        "gemm": lambda s: ep.ep_expert_gemm_fp8(a, a_s, d13["q"], d13["scale"], off, stream=s),
+        "swiglu": lambda s: ep.ep_expert_swiglu_fp8(a, a_s, d13["q"], d13["scale"], off,
+                                                    save_gate_up=True, stream=s),
+        "swiglu_grad": lambda s: ep.ep_swiglu_grad(dh, gu, stream=s),
+        "wgrad": lambda s: ep.ep_expert_wgrad(gu, a.view(torch.uint8).to(torch.bfloat16), off, stream=s),
+        "wgrad_parts": lambda s: ep.ep_expert_wgrad(rows, rows, one, stream=s),
+        "moe_tokens": lambda s: ep.ep_moe_tokens(x, idx, tw, w13, w2, stream=s),
+        "moe_tokens_fp8": lambda s: ep.ep_moe_tokens(x, idx, tw, d13["q"], d2["q"], d13["scale"],
+                                                     d2["scale"], stream=s),
+    }
+
+
+NAMES = ["quantize", "dispatch_fp8", "quantize_weight", "gemm", "swiglu", "swiglu_grad", "wgrad",
+         "wgrad_parts", "moe_tokens", "moe_tokens_fp8"]
+
+
+@pytest.mark.parametrize("handle", ["stream", "integer"])
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_belong_to_the_calls_stream(ep, name, handle):
+    call = calls(ep)[name]
+    want = [t.clone() for t in tensors(call(None))]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    say(f"{name} on another stream ({handle})")
+    got = tensors(call(s if handle == "stream" else s.cuda_stream))
+    torch.cuda.synchronize()
+    assert len(got) == len(want) > 0
+    for a, b in zip(got, want):
+        assert pool_of(a) == s.cuda_stream, name
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_null_stream_from_another_current_one(ep, name):
+    call = calls(ep)[name]
+    torch.cuda.synchronize()
+    say(f"{name} on the null stream")
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = tensors(call(0))
+    torch.cuda.synchronize()
+    assert got and all(pool_of(t) == 0 for t in got)
+
+
+@pytest.mark.parametrize("name", ["gemm", "moe_tokens", "swiglu_grad", "quantize"])
+def test_pending_work_of_the_current_stream(ep, name):
+    """A block that a write still waits for on the current stream, dropped by its owner, is not handed
+    to a call on another stream."""
+    call = calls(ep)[name]
+    want = [t.clone() for t in tensors(call(None))]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    say(f"{name} beside pending writes")
+    blocks = [torch.empty(t.numel() * t.element_size(), dtype=torch.uint8, device=DEV) for t in want]
+    torch.cuda._sleep(20_000_000)
+    for b in blocks:
+        b.fill_(0x5A)
+    del blocks, b
+    got = tensors(call(s))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
