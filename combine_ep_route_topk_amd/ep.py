@@ -8,8 +8,8 @@ pre-allocated (the benchmark does) or are allocated here with torch.empty.
 
 `stream` (a torch stream or a raw handle; default: the current one) is the
 stream that a call's kernels run on.  As in a `with torch.cuda.stream(stream)`
-block, what an expert operator allocates belongs to that stream, and the caller
-orders the rest: tensors passed in are ready on it, and they, like results used
+block, what a call allocates belongs to that stream, and the caller orders the
+rest: tensors passed in are ready on it, and they, like results used
 on other streams, are not dropped before the work that uses them is done
 (Tensor.record_stream, or a wait).
 
@@ -18,6 +18,7 @@ missing: there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -139,13 +140,19 @@ def _stream_object(stream, dev) -> torch.cuda.Stream:
             else torch.cuda.default_stream(dev))
 
 
+def _on(stream, dev):
+    """Within it, allocations and work on the default stream argument belong to `stream`."""
+    return (contextlib.nullcontext() if stream is None
+            else torch.cuda.stream(_stream_object(stream, dev)))
+
+
 def _empty(shape, dtype: torch.dtype, dev, stream) -> torch.Tensor:
     """An output or a workspace made inside a call, from the memory of the stream that the call runs
     on.  From another stream's, the block may be one that work pending there still uses, and the
     allocator would hand it out there again, once it is dropped, while the call still runs."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(_stream_object(stream, dev)):
+    with _on(stream, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
@@ -182,9 +189,9 @@ def ep_route_topk(logits: torch.Tensor, k: int, normalize: bool = True,
     T, E = logits.shape
     dev = logits.device
     if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_idx = _empty((T, k), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        topk_w = _empty((T, k), torch.float32, dev, stream)
     _need(topk_idx, "topk_idx", torch.int32, (T, k))
     _need(topk_w, "topk_w", torch.float32, (T, k))
     _check(_lib.ep_route_topk(_ptr(logits), T, E, k, int(bool(normalize)), _ptr(topk_idx),
@@ -217,7 +224,8 @@ def ep_dispatch_layout(topk_idx: torch.Tensor, E: int, R: int, out: dict | None 
     T, k = topk_idx.shape
     dev = topk_idx.device
     if out is None:
-        out = layout_outputs(T, k, E, R, dev)
+        with _on(stream, dev):
+            out = layout_outputs(T, k, E, R, dev)
     ws = out["workspace"]
     _need(ws, "workspace", torch.uint8)
     for name, shape in (("expert_counts", (E,)), ("expert_offsets", (E + 1,)),
@@ -262,7 +270,7 @@ def ep_dispatch(x: torch.Tensor, pos: torch.Tensor, send: torch.Tensor | None = 
     if pos.shape[0] != T:
         raise ValueError("pos must be [T][k]")
     if send is None:
-        send = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+        send = _empty((T * k, H), x.dtype, x.device, stream)
     _bits_ok(send, "send", (T * k, H))
     _check(_lib.ep_dispatch(_ptr(x), T, H, k, _ptr(pos), _ptr(send),
                             _P(_stream(stream, x.device))))
@@ -281,7 +289,7 @@ def ep_combine(y: torch.Tensor, pos: torch.Tensor, topk_w: torch.Tensor,
         raise ValueError("y must have T*k rows")
     _need(topk_w, "topk_w", torch.float32, (T, k))
     if out is None:
-        out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+        out = _empty((T, H), y.dtype, y.device, stream)
     _bits_ok(out, "out", (T, H))
     _check(_lib.ep_combine(_ptr(y), _ptr(pos), _ptr(topk_w), T, H, k, _ptr(out),
                            _P(_stream(stream, y.device))))
@@ -303,9 +311,9 @@ def ep_combine_grad(grad_out: torch.Tensor, y: torch.Tensor, pos: torch.Tensor,
     _bits_ok(y, "y", (T * k, H))
     _need(topk_w, "topk_w", torch.float32, (T, k))
     if grad_y is None:
-        grad_y = torch.empty((T * k, H), dtype=y.dtype, device=y.device)
+        grad_y = _empty((T * k, H), y.dtype, y.device, stream)
     if grad_w is None:
-        grad_w = torch.empty((T, k), dtype=torch.float32, device=y.device)
+        grad_w = _empty((T, k), torch.float32, y.device, stream)
     _bits_ok(grad_y, "grad_y", (T * k, H))
     _need(grad_w, "grad_w", torch.float32, (T, k))
     _check(_lib.ep_combine_grad(_ptr(grad_out), _ptr(y), _ptr(pos), _ptr(topk_w), T, H, k,
@@ -323,7 +331,7 @@ def ep_dispatch_grad(grad_send: torch.Tensor, pos: torch.Tensor,
     if grad_send.shape[0] != T * k:
         raise ValueError("grad_send must have T*k rows")
     if grad_x is None:
-        grad_x = torch.empty((T, H), dtype=grad_send.dtype, device=grad_send.device)
+        grad_x = _empty((T, H), grad_send.dtype, grad_send.device, stream)
     _bits_ok(grad_x, "grad_x", (T, H))
     _check(_lib.ep_dispatch_grad(_ptr(grad_send), _ptr(pos), T, H, k, _ptr(grad_x),
                                  _P(_stream(stream, grad_send.device))))
@@ -375,7 +383,8 @@ def ep_fused_dispatch_combine(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: t
     k = topk_idx.shape[1]
     _need(topk_w, "topk_w", torch.float32, (T, k))
     if out is None:
-        out = fused_outputs(T, H, k, E, R, x.device)
+        with _on(stream, x.device):      # the workspace's initialisation with it
+            out = fused_outputs(T, H, k, E, R, x.device)
     st = _stream(stream, x.device)
     if sync == EP_FUSED_SYNC_ITEM_EVENTS and not spin_limit:
         _check(_lib.ep_fused_dispatch_combine(
@@ -418,9 +427,9 @@ def ep_expert_slices(expert_offsets: torch.Tensor, P: int, out: dict | None = No
     E = expert_offsets.numel() - 1
     dev = expert_offsets.device
     if out is None:
-        out = dict(start=torch.empty(P + 1, dtype=torch.int64, device=dev),
-                   expert=torch.empty(P, dtype=torch.int32, device=dev),
-                   offset=torch.empty(P, dtype=torch.int64, device=dev))
+        out = dict(start=_empty(P + 1, torch.int64, dev, stream),
+                   expert=_empty(P, torch.int32, dev, stream),
+                   offset=_empty(P, torch.int64, dev, stream))
     _need(out["start"], "start", torch.int64, (P + 1,))
     _need(out["expert"], "expert", torch.int32, (P,))
     _need(out["offset"], "offset", torch.int64, (P,))
@@ -452,7 +461,8 @@ def ep_rank_coalesce(topk_idx: torch.Tensor, E: int, R: int, out: dict | None = 
     T, k = topk_idx.shape
     dev = topk_idx.device
     if out is None:
-        out = coalesce_outputs(T, k, E, R, dev)
+        with _on(stream, dev):
+            out = coalesce_outputs(T, k, E, R, dev)
     ws = out["workspace"]
     _need(ws, "workspace", torch.uint8)
     for name, shape in (("rank_counts", (R,)), ("rank_offsets", (R + 1,)),
@@ -477,12 +487,11 @@ def ep_expand_records(rows: torch.Tensor, masks: torch.Tensor, L: int, recv_rows
     _need(masks, "masks", torch.int64, (C,))
     dev = rows.device
     if out is None:
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = dict(expert_counts=torch.empty(L, **i32), expert_offsets=torch.empty(L + 1, **i32),
-                   pos=torch.empty((C, L), **i32),
-                   recv=torch.empty((recv_rows, H), dtype=rows.dtype, device=dev),
-                   workspace=torch.empty(int(_lib.ep_expand_records_workspace_bytes(C, L)),
-                                         dtype=torch.uint8, device=dev))
+        i32 = (torch.int32, dev, stream)
+        out = dict(expert_counts=_empty(L, *i32), expert_offsets=_empty(L + 1, *i32),
+                   pos=_empty((C, L), *i32), recv=_empty((recv_rows, H), rows.dtype, dev, stream),
+                   workspace=_empty(int(_lib.ep_expand_records_workspace_bytes(C, L)), torch.uint8,
+                                    dev, stream))
     _need(out["expert_counts"], "expert_counts", torch.int32, (L,))
     _need(out["expert_offsets"], "expert_offsets", torch.int32, (L + 1,))
     _need(out["pos"], "pos", torch.int32, (C, L))

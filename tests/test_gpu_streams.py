@@ -52,6 +52,7 @@ def calls(ep):
     a, a_s = ep.ep_dispatch_fp8(x, pos)
     gu, dh = normal(g, T * k, 2 * I), normal(g, T * k, I)
     rows = normal(g, 4096, 256)
+    y, masks = normal(g, T * k, H), torch.arange(T, device=DEV) % 16
     one = torch.tensor([0, 4096], dtype=torch.int32, device=DEV)
     return {
         "quantize": lambda s: ep.ep_quantize_fp8(x, stream=s),
@@ -66,30 +67,50 @@ def calls(ep):
         "moe_tokens": lambda s: ep.ep_moe_tokens(x, idx, tw, w13, w2, stream=s),
         "moe_tokens_fp8": lambda s: ep.ep_moe_tokens(x, idx, tw, d13["q"], d2["q"], d13["scale"],
                                                      d2["scale"], stream=s),
+        "route": lambda s: ep.ep_route_topk(logits, k, stream=s),
+        "layout": lambda s: ep.ep_dispatch_layout(idx, E, 2, stream=s),
+        "dispatch": lambda s: ep.ep_dispatch(x, pos, stream=s),
+        "combine": lambda s: ep.ep_combine(y, pos, tw, stream=s),
+        "combine_grad": lambda s: ep.ep_combine_grad(x, y, pos, tw, stream=s),
+        "dispatch_grad": lambda s: ep.ep_dispatch_grad(y, pos, stream=s),
+        "fused": lambda s: ep.ep_fused_dispatch_combine(x, idx, tw, E, 2, stream=s),
+        "slices": lambda s: ep.ep_expert_slices(off, 3, stream=s),
+        "coalesce": lambda s: ep.ep_rank_coalesce(idx, E, 2, stream=s),
+        "expand": lambda s: ep.ep_expand_records(x, masks, E, T * E, stream=s),
     }
+
+
+def known(v):
+    """Without what a call leaves undefined in part: workspaces, row tails, rows behind the last."""
+    if not isinstance(v, dict):
+        return tensors(v)
+    return [t for n, t in v.items()
+            if n not in ("workspace", "send_rows", "row_src", "row_experts", "recv")]
 
 
 NAMES = ["quantize", "dispatch_fp8", "quantize_weight", "gemm", "swiglu", "swiglu_grad", "wgrad",
          "wgrad_parts", "moe_tokens", "moe_tokens_fp8"]
+EARLIER = ["route", "layout", "dispatch", "combine", "combine_grad", "dispatch_grad", "fused", "slices",
+           "coalesce", "expand"]
 
 
 @pytest.mark.parametrize("handle", ["stream", "integer"])
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", NAMES + EARLIER)
 def test_outputs_belong_to_the_calls_stream(ep, name, handle):
     call = calls(ep)[name]
-    want = [t.clone() for t in tensors(call(None))]
+    want = [t.clone() for t in known(call(None))]
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     say(f"{name} on another stream ({handle})")
-    got = tensors(call(s if handle == "stream" else s.cuda_stream))
+    got = call(s if handle == "stream" else s.cuda_stream)
     torch.cuda.synchronize()
-    assert len(got) == len(want) > 0
-    for a, b in zip(got, want):
-        assert pool_of(a) == s.cuda_stream, name
+    assert all(pool_of(t) == s.cuda_stream for t in tensors(got)), name
+    assert len(known(got)) == len(want) > 0
+    for a, b in zip(known(got), want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
 
 
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", NAMES + EARLIER)
 def test_null_stream_from_another_current_one(ep, name):
     call = calls(ep)[name]
     torch.cuda.synchronize()
@@ -100,7 +121,8 @@ def test_null_stream_from_another_current_one(ep, name):
     assert got and all(pool_of(t) == 0 for t in got)
 
 
-@pytest.mark.parametrize("name", ["gemm", "moe_tokens", "swiglu_grad", "quantize"])
+@pytest.mark.parametrize("name", ["gemm", "moe_tokens", "swiglu_grad", "quantize", "dispatch", "combine",
+                                  "dispatch_grad", "route"])
 def test_pending_work_of_the_current_stream(ep, name):
     """A block that a write still waits for on the current stream, dropped by its owner, is not handed
     to a call on another stream."""
