@@ -122,12 +122,16 @@ def ep_abi_version() -> int:
     return _lib.ep_abi_version()
 
 
-_current_stream = torch._C._cuda_getCurrentRawStream
+# The current stream's handle alone (a Stream object takes 2 us to make), where torch offers it:
+# a build without GPU support does not, and this module loads there too.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, device) -> int:
-    if stream is None:        # the handle alone: a Stream object takes 2 us to make
-        return _current_stream(device.index)
+    if stream is None:
+        if _current_handle is None:
+            return torch.cuda.current_stream(device).cuda_stream
+        return _current_handle(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
