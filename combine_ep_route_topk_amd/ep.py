@@ -739,8 +739,9 @@ def ep_expert_swiglu_fp8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tens
 
 def ep_swiglu_grad(grad_h: torch.Tensor, gate_up: torch.Tensor,
                    grad_gate_up: torch.Tensor | None = None, h: torch.Tensor | None = None,
-                   stream=None):
-    """grad_h bf16 [S][I], gate_up bf16 [S][2I] -> (grad_gate_up bf16 [S][2I], h bf16 [S][I])."""
+                   save_h: bool = True, stream=None):
+    """grad_h bf16 [S][I], gate_up bf16 [S][2I] -> (grad_gate_up bf16 [S][2I], h bf16 [S][I] or
+    None).  h is written when it is passed in or save_h is true (a sixth of the bytes)."""
     S, I = _shape(grad_h, "grad_h", 2)
     _bits_ok(grad_h, "grad_h")
     _bits_ok(gate_up, "gate_up", (S, 2 * I))
@@ -749,9 +750,9 @@ def ep_swiglu_grad(grad_h: torch.Tensor, gate_up: torch.Tensor,
         grad_gate_up = _empty((S, 2 * I), gate_up.dtype, dev, stream)
     else:
         _bits_ok(grad_gate_up, "grad_gate_up", (S, 2 * I))
-    if h is None:
+    if h is None and save_h:
         h = _empty((S, I), grad_h.dtype, dev, stream)
-    else:
+    elif h is not None:
         _bits_ok(h, "h", (S, I))
     _launch(_lib.ep_swiglu_grad, dev, stream, (gate_up, grad_gate_up, h), _ptr(grad_h),
             _ptr(gate_up), S, I, _ptr(grad_gate_up), _ptr(h))
