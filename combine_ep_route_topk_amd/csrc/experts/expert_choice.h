@@ -1,0 +1,95 @@
+// expert_choice.h -- which kernel a grouped product or a weight gradient takes.
+// Host rules on sizes alone, in a header of their own so that a test can ask
+// which kernel its sizes reach.
+#pragma once
+
+#include <stdint.h>
+
+namespace ep {
+
+// ------------------------------------------------------------- grouped products
+// The persistent 256 x 256 kernel, or the kernel for few rows with tiles of so
+// many tokens x weight rows.
+enum GemmKernel {
+    kGemmLarge,
+    kGemm128x256,
+    kGemm64x256,
+    kGemm32x256,
+    kGemm128x128,
+    kGemm64x128,
+    kGemm32x64,
+};
+
+// Which kernel, by the rows an expert has on average and the workgroups that a
+// tile would make.  Measured on MI355X, us for 64 / 128-row tiles / the large ones:
+//   8 experts x 4096 x 7168, rows each   48: 50 / 59 / 77    96: 91 / 72 / 81
+//                                       160: 133 / 97 / 85  192: 142 / 101 / 89
+//   16 x 2816 x 4096                     48: 44 / 40 / 52   128: 75 / 50 / 60
+//   1 x 4096 x 4096                    1024: 38 / 40 / 48  2048: 68 / 52 / 51
+//   4 x 2048 x 4096                     256: 30 / 39 / 48   512: 38 / 40 / 49
+// With few rows the weights are read at the rate of the busiest CU, so as near to
+// one workgroup each as can be; us for 256 / 128 / 64 weight rows a workgroup:
+//   16 experts x 2816 x 4096, 30 rows each  36 / 41 / 38
+//   8 x 4096 x 7168, 32 rows                56 / 44 / 45
+//   2 x 4096 x 7168, 8 rows                 29 / 23 / 20
+//   32 x 4096 x 7168, 16 rows              161 / 160 / 165
+// With 256 weight rows (gated always), 64 / 32 tokens a workgroup, gated:
+//   8 x 4096 x 7168, 48 rows 55 / 50;  1 x 4096 x 7168, 64 rows 39 / 31;  4 x 1024 x
+//   2048, 300 rows 17 / 14;  16 x 2816 x 4096, 30 rows 34 / 33, 45 rows 35 / 53;
+//   32 x 4096 x 4096, 48 rows 94 / 130
+// One workgroup a CU has room for 128 rows: where the 32 rows are an average, of 94
+// to 12, 53 us instead of 64.
+// N: rows of one expert's weights (2 I when gated).
+inline GemmKernel choose_gemm(int64_t S, int64_t N, int64_t E, bool gated, int64_t cus)
+{
+    auto tiles = [&](int64_t tm, int64_t tn) {
+        const int64_t mt = (S + tm - 1) / tm;
+        return (mt > E ? mt : E) * ((N + tn - 1) / tn);
+    };
+    if (S >= 160 * E && tiles(256, 256) >= 112) return kGemmLarge;
+    if (S > 48 * E && tiles(128, 256) > 128) return kGemm128x256;
+    if (!gated) {
+        const int64_t wide = tiles(64, 256);
+        if (wide > cus || wide * 3 < cus * 2) {
+            if (tiles(32, 64) <= cus) return kGemm32x64;
+            if (tiles(128, 128) <= cus) return kGemm128x128;
+            return kGemm64x128;
+        }
+    }
+    // a last, partly filled tile for every other expert
+    const int64_t few = (S / 32 + E / 2) * ((N + 255) / 256);
+    return few <= cus ? kGemm32x256 : kGemm64x256;
+}
+
+// ------------------------------------------------------------- weight gradients
+constexpr int kWgradTile = 256, kWgradSmallTile = 128;
+
+inline int64_t wgrad_tiles(int N, int K, int E, int tile)
+{
+    return int64_t((N + tile - 1) / tile) * ((K + tile - 1) / tile) * E;
+}
+
+// Large tiles want a whole round of them and rows enough to hide their stores
+// (16 experts x 2816 x 4096, large / small tiles: 128 rows each 145 / 133 us, 176
+// rows 170 / 170, 256 rows 169 / 186; 8 experts x 1024 x 1024, half a round: 35 / 31).
+inline bool wgrad_large(int S, int N, int K, int E)
+{
+    return wgrad_tiles(N, K, E, kWgradTile) >= 256 && S >= int64_t(192) * E;
+}
+
+// Parts that an expert's rows are split into: 1, unless there are few small
+// tiles (up to 192, towards 768 workgroups) and rows for several parts of 128.
+// 32768 rows, 256 x 512 (8 tiles): 372 us whole, 37 in 64 parts; 4 experts of 4096
+// rows, 512 x 512 (64 tiles): 54, 29 in 12; 8 of 4096, 512 x 1024 (256): 61, 70 in 3.
+// From sizes alone, so that a workspace's size holds on every device.
+inline int wgrad_parts(int S, int N, int K, int E)
+{
+    if (wgrad_large(S, N, K, E)) return 1;
+    const int64_t tiles = wgrad_tiles(N, K, E, kWgradSmallTile);
+    if (tiles > 192) return 1;
+    const int64_t most = 768 / tiles, rows = S / (int64_t(128) * E);
+    const int64_t parts = most < rows ? most : rows;
+    return parts < 2 ? 1 : parts > 64 ? 64 : int(parts);
+}
+
+}  // namespace ep

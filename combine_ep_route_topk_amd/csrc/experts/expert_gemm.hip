@@ -14,6 +14,7 @@
 // Segments of many rows are bound by matrix work and take the kernel of
 // expert_gemm_large.h; the one here is for few rows, where the weights' bytes
 // bound it.
+#include "expert_choice.h"
 #include "expert_gemm_large.h"
 
 namespace ep {
@@ -266,48 +267,26 @@ hipError_t launch_large(GemmArgs p, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which kernel, by the rows an expert has on average and the workgroups that a
-// tile would make.  Measured on MI355X, us for 64 / 128-row tiles / the large ones:
-//   8 experts x 4096 x 7168, rows each   48: 50 / 59 / 77    96: 91 / 72 / 81
-//                                       160: 133 / 97 / 85  192: 142 / 101 / 89
-//   16 x 2816 x 4096                     48: 44 / 40 / 52   128: 75 / 50 / 60
-//   1 x 4096 x 4096                    1024: 38 / 40 / 48  2048: 68 / 52 / 51
-//   4 x 2048 x 4096                     256: 30 / 39 / 48   512: 38 / 40 / 49
-// With few rows the weights are read at the rate of the busiest CU, so as near to
-// one workgroup each as can be; us for 256 / 128 / 64 weight rows a workgroup:
-//   16 experts x 2816 x 4096, 30 rows each  36 / 41 / 38
-//   8 x 4096 x 7168, 32 rows                56 / 44 / 45
-//   2 x 4096 x 7168, 8 rows                 29 / 23 / 20
-//   32 x 4096 x 7168, 16 rows              161 / 160 / 165
-// With 256 weight rows (gated always), 64 / 32 tokens a workgroup, gated:
-//   8 x 4096 x 7168, 48 rows 55 / 50;  1 x 4096 x 7168, 64 rows 39 / 31;  4 x 1024 x
-//   2048, 300 rows 17 / 14;  16 x 2816 x 4096, 30 rows 34 / 33, 45 rows 35 / 53;
-//   32 x 4096 x 4096, 48 rows 94 / 130
-// One workgroup a CU has room for 128 rows: where the 32 rows are an average, of 94
-// to 12, 53 us instead of 64.
 template <bool GATED>
 hipError_t launch(const GemmArgs& p, hipStream_t s)
 {
-    const int64_t cus = device_cu_count();
-    auto tiles = [&](int TM, int TN) {
-        const int64_t mt = (int64_t(p.S) + TM - 1) / TM;
-        return (mt > p.E ? mt : p.E) * ((p.N + TN - 1) / TN);
-    };
-    if (p.S >= int64_t(160) * p.E && tiles(kLargeTile, 256) >= 112) return launch_large<GATED>(p, s);
-    if (p.S > int64_t(48) * p.E && tiles(128, 256) > 128)
-        return launch_stream<128, 8, 32, GATED>(p, s);
+    const GemmKernel kernel = choose_gemm(p.S, p.N, p.E, GATED, device_cu_count());
+    switch (kernel) {
+        case kGemmLarge: return launch_large<GATED>(p, s);
+        case kGemm128x256: return launch_stream<128, 8, 32, GATED>(p, s);
+        case kGemm64x256: return launch_stream<64, 8, 32, GATED>(p, s);
+        case kGemm32x256: return launch_stream<32, 8, 32, GATED>(p, s);
+        default: break;
+    }
     if constexpr (!GATED) {
-        const int64_t wide = tiles(64, 256);
-        if (wide > cus || wide * 3 < cus * 2) {
-            if (tiles(32, 64) <= cus) return launch_stream<32, 4, 16, false>(p, s);
-            if (tiles(128, 128) <= cus) return launch_stream<128, 4, 32, false>(p, s);
-            return launch_stream<64, 4, 32, false>(p, s);
+        switch (kernel) {
+            case kGemm128x128: return launch_stream<128, 4, 32, false>(p, s);
+            case kGemm64x128: return launch_stream<64, 4, 32, false>(p, s);
+            case kGemm32x64: return launch_stream<32, 4, 16, false>(p, s);
+            default: break;
         }
     }
-    // a last, partly filled tile for every other expert
-    const int64_t few = (int64_t(p.S) / 32 + p.E / 2) * ((p.N + 255) / 256);
-    if (few <= cus) return launch_stream<32, 8, 32, GATED>(p, s);
-    return launch_stream<64, 8, 32, GATED>(p, s);
+    return hipErrorInvalidConfiguration;
 }
 
 }  // namespace

@@ -7,6 +7,7 @@
 // through its transposing 16-bit read.  x is the row operand: a lane ends up
 // with four neighbouring j of one i, 16-byte stores.  Rows past the segment lie
 // outside the load descriptors and read as zero.
+#include "expert_choice.h"
 #include "experts_internal.h"
 
 namespace ep {
@@ -98,7 +99,7 @@ __device__ __forceinline__ void put_fragments(__amdgpu_buffer_rsrc_t r, uint8_t*
 // LDS image of a stage: rows of 512 bytes in units of 64, unit u of row r at
 // u ^ r % 4: a transposing read takes 8 rows x 64 bytes, rows 0..3 and 8..11 of
 // 16, which then touch every bank twice, the least that 512 bytes can.
-constexpr int kTile = 256, kRows = 64;
+constexpr int kTile = kWgradTile, kRows = 64;
 constexpr int kStage = kRows * kTile * 2;            // 32 KB of one operand
 constexpr int kLoads = kStage / 16 / 256;            // 8 of 16 bytes a thread
 
@@ -328,7 +329,7 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
 // of a row of the output run together (column by column: 64 rows each 149 us, 133).  With few tiles
 // each expert's rows are split over `parts` workgroups a tile, whose sums go to
 // a workspace [part][E][N][K] and are joined in order by a second launch.
-constexpr int kSmallTile = 128, kSmallRows = 32;
+constexpr int kSmallTile = kWgradSmallTile, kSmallRows = 32;
 constexpr int kSmallStage = 2 * kSmallRows * kSmallTile * 2;      // dy, then x: 16 KB
 
 template <bool ACC, bool NT>
@@ -483,35 +484,7 @@ hipError_t launch_small(WgradArgs p, int parts, bool accumulate, float* sums, hi
     return hipGetLastError();
 }
 
-int64_t wgrad_tiles(int N, int K, int E, int tile)
-{
-    return int64_t((N + tile - 1) / tile) * ((K + tile - 1) / tile) * E;
-}
-
-// Large tiles want a whole round of them and rows enough to hide their stores
-// (16 experts x 2816 x 4096, large / small tiles: 128 rows each 145 / 133 us, 176
-// rows 170 / 170, 256 rows 169 / 186; 8 experts x 1024 x 1024, half a round: 35 / 31).
-bool wgrad_large(int S, int N, int K, int E)
-{
-    return wgrad_tiles(N, K, E, kTile) >= 256 && S >= int64_t(192) * E;
-}
-
 }  // namespace
-
-// Parts that an expert's rows are split into: 1, unless there are few small
-// tiles (up to 192, towards 768 workgroups) and rows for several parts of 128.
-// 32768 rows, 256 x 512 (8 tiles): 372 us whole, 37 in 64 parts; 4 experts of 4096
-// rows, 512 x 512 (64 tiles): 54, 29 in 12; 8 of 4096, 512 x 1024 (256): 61, 70 in 3.
-// From sizes alone, so that a workspace's size holds on every device.
-int wgrad_parts(int S, int N, int K, int E)
-{
-    if (wgrad_large(S, N, K, E)) return 1;
-    const int64_t tiles = wgrad_tiles(N, K, E, kSmallTile);
-    if (tiles > 192) return 1;
-    const int64_t most = 768 / tiles, rows = S / (int64_t(128) * E);
-    const int64_t parts = most < rows ? most : rows;
-    return parts < 2 ? 1 : parts > 64 ? 64 : int(parts);
-}
 
 hipError_t launch_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32_t* offsets,
                                int S, int N, int K, int E, int accumulate, float* grad_w,

@@ -1,6 +1,7 @@
 // experts_api.hip -- the extern "C" entry points of the expert operators
 // (include/ep_route_topk.h): argument validation, then kernel launches.
 #include "../ep_api.h"
+#include "expert_choice.h"
 #include "experts_internal.h"
 
 namespace {

@@ -34,7 +34,6 @@ hipError_t launch_expert_swiglu(const uint8_t* a, const uint8_t* a_scale, const 
 hipError_t launch_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32_t* offsets,
                                int S, int N, int K, int E, int accumulate, float* grad_w,
                                float* sums, hipStream_t s);
-int wgrad_parts(int S, int N, int K, int E);
 hipError_t launch_swiglu_grad(const uint16_t* grad_h, const uint16_t* gate_up, int S, int I,
                               uint16_t* grad_gate_up, uint16_t* h, hipStream_t s);
 size_t moe_tokens_workspace(int T, int k, int I);
