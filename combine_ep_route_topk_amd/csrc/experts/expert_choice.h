@@ -38,13 +38,18 @@ enum GemmKernel {
 //   2048, 300 rows 17 / 14;  16 x 2816 x 4096, 30 rows 34 / 33, 45 rows 35 / 53;
 //   32 x 4096 x 4096, 48 rows 94 / 130
 // One workgroup a CU has room for 128 rows: where the 32 rows are an average, of 94
-// to 12, 53 us instead of 64.
+// to 12, 53 us instead of 64; of 64 rows at most in all there is nothing to hold
+// (8 rows over 64 experts x 4096 x 7168: 37.6, with 64 36.7).
+// At most S experts have rows.  All of them counted / those, 7168 values of k: 8 rows
+// over 64 experts x 2048 29.9 / 25.9, 8 over 16 x 4096 46.5 / 36.1, 3 over 8 x 4096
+// 30.7 / 24.6, 1 over 64 x 4096 27.2 / 23.0.
 // N: rows of one expert's weights (2 I when gated).
 inline GemmKernel choose_gemm(int64_t S, int64_t N, int64_t E, bool gated, int64_t cus)
 {
+    const int64_t used = S < E ? S : E;         // experts that can have rows
     auto tiles = [&](int64_t tm, int64_t tn) {
         const int64_t mt = (S + tm - 1) / tm;
-        return (mt > E ? mt : E) * ((N + tn - 1) / tn);
+        return (mt > used ? mt : used) * ((N + tn - 1) / tn);
     };
     if (S >= 160 * E && tiles(256, 256) >= 112) return kGemmLarge;
     if (S > 48 * E && tiles(128, 256) > 128) return kGemm128x256;
@@ -52,12 +57,12 @@ inline GemmKernel choose_gemm(int64_t S, int64_t N, int64_t E, bool gated, int64
         const int64_t wide = tiles(64, 256);
         if (wide > cus || wide * 3 < cus * 2) {
             if (tiles(32, 64) <= cus) return kGemm32x64;
-            if (tiles(128, 128) <= cus) return kGemm128x128;
+            if (S > 64 && tiles(128, 128) <= cus) return kGemm128x128;
             return kGemm64x128;
         }
     }
     // a last, partly filled tile for every other expert
-    const int64_t few = (S / 32 + E / 2) * ((N + 255) / 256);
+    const int64_t few = (S / 32 + used / 2) * ((N + 255) / 256);
     return few <= cus ? kGemm32x256 : kGemm64x256;
 }
 
