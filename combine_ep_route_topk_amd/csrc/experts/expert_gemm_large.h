@@ -35,8 +35,6 @@
 namespace ep {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 struct GemmArgs {
     const uint8_t* a;
     const uint8_t* a_scale;
@@ -105,30 +103,6 @@ struct GemmTiles {
         return t;
     }
 };
-
-// Waits until at most VM of this wave's vector-memory operations and none of
-// its LDS reads are outstanding, then for the workgroup.
-template <int VM>
-__device__ __forceinline__ void wait_and_barrier() {
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-}
-
-// Keeps a matrix instruction's result, and so the instruction, in its place.
-__device__ __forceinline__ void pin(f32x16& v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("" : "+a"(v));
-#endif
-}
-
-// Makes a value look new, so that nothing computed from it is moved before.
-__device__ __forceinline__ void hide(int& v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("" : "+v"(v));
-#endif
-}
 
 constexpr int kLargeTile = 256;
 

@@ -13,7 +13,6 @@
 namespace ep {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 struct WgradArgs {
@@ -102,24 +101,6 @@ __device__ __forceinline__ void put_fragments(__amdgpu_buffer_rsrc_t r, uint8_t*
 constexpr int kTile = kWgradTile, kRows = 64;
 constexpr int kStage = kRows * kTile * 2;            // 32 KB of one operand
 constexpr int kLoads = kStage / 16 / 256;            // 8 of 16 bytes a thread
-
-template <int VM>
-__device__ __forceinline__ void wait_and_barrier() {
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-}
-__device__ __forceinline__ void pin(f32x16& v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("" : "+a"(v));
-#endif
-}
-__device__ __forceinline__ void hide(int& v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("" : "+v"(v));
-#endif
-}
 
 struct WgradTile {
     int expert, i0, j0, begin, end;      // expert -1: none

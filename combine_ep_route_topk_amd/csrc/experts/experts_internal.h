@@ -46,6 +46,7 @@ hipError_t launch_moe_tokens(const uint16_t* x, const int32_t* idx, const float*
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -101,6 +102,31 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ s16x4 read_transposed(uint8_t* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) s16x4*)(p));
+}
+
+// ----------------------------------------------------------------- order
+// Waits until at most VM of this wave's vector-memory operations and none of
+// its LDS reads are outstanding, then for the workgroup.
+template <int VM>
+__device__ __forceinline__ void wait_and_barrier() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// Keeps a matrix instruction's result, and so the instruction, in its place.
+__device__ __forceinline__ void pin(f32x16& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+a"(v));
+#endif
+}
+
+// Makes a value look new, so that nothing computed from it is moved before.
+__device__ __forceinline__ void hide(int& v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(v));
+#endif
 }
 
 // ----------------------------------------------------------------- segments
