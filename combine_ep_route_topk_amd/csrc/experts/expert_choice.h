@@ -21,28 +21,34 @@ enum GemmKernel {
 };
 
 // Which kernel, by the rows an expert has on average and the workgroups that a
-// tile would make.  Measured on MI355X, us for 64 / 128-row tiles / the large ones:
-//   8 experts x 4096 x 7168, rows each   48: 50 / 59 / 77    96: 91 / 72 / 81
-//                                       160: 133 / 97 / 85  192: 142 / 101 / 89
-//   16 x 2816 x 4096                     48: 44 / 40 / 52   128: 75 / 50 / 60
-//   1 x 4096 x 4096                    1024: 38 / 40 / 48  2048: 68 / 52 / 51
-//   4 x 2048 x 4096                     256: 30 / 39 / 48   512: 38 / 40 / 49
+// tile would make.  Measured on MI355X with weights that come from memory, even rows,
+// us for 64 / 128 tokens x 256 weight rows / the large kernel:
+//   8 experts x 4096 x 7168, rows each   48: 53 / 55 / 74    96: 53 / 64 / 75
+//                                       160: 98 / 83 / 79   192: 101 / 83 / 82
+//   16 x 2816 x 4096                     48: 34 / 35 / 51   128: 59 / 45 / 55   160: 87 / 87 / 56
+//   1 x 4096 x 4096                    1024: 26 / 38 / 46  2048: 52 / 41 / 47
+//   4 x 2048 x 4096                     256: 28 / 40 / 50   512: 28 / 40 / 50
+//   32 x 2816 x 4096                    128: 98 / 91 / 113  256: 167 / 131 / 126
 // With few rows the weights are read at the rate of the busiest CU, so as near to
 // one workgroup each as can be; us for 256 / 128 / 64 weight rows a workgroup:
-//   16 experts x 2816 x 4096, 30 rows each  36 / 41 / 38
-//   8 x 4096 x 7168, 32 rows                56 / 44 / 45
-//   2 x 4096 x 7168, 8 rows                 29 / 23 / 20
-//   32 x 4096 x 7168, 16 rows              161 / 160 / 165
+//   16 experts x 2816 x 4096, 30 rows each  32 / 38 / 33
+//   8 x 4096 x 7168, 32 rows                51 / 39 / 39
+//   2 x 4096 x 7168, 8 rows                 42 / 29 / 24
+//   32 x 4096 x 7168, 16 rows              145 / 143 / 145
 // With 256 weight rows (gated always), 64 / 32 tokens a workgroup, gated:
-//   8 x 4096 x 7168, 48 rows 55 / 50;  1 x 4096 x 7168, 64 rows 39 / 31;  4 x 1024 x
-//   2048, 300 rows 17 / 14;  16 x 2816 x 4096, 30 rows 34 / 33, 45 rows 35 / 53;
-//   32 x 4096 x 4096, 48 rows 94 / 130
+//   8 x 4096 x 7168, 48 rows 54 / 49, 96 rows 52 / 92;  1 x 4096 x 7168, 64 rows 48 /
+//   42;  4 x 1024 x 2048, 300 rows 16 / 13;  16 x 2816 x 4096, 30 rows 32 / 32, 45 rows
+//   34 / 52;  32 x 4096 x 4096, 48 rows 89 / 116
 // One workgroup a CU has room for 128 rows: where the 32 rows are an average, of 94
-// to 12, 53 us instead of 64; of 64 rows at most in all there is nothing to hold
+// to 12, 45 us instead of 62; of 64 rows at most in all there is nothing to hold
 // (8 rows over 64 experts x 4096 x 7168: 37.6, with 64 36.7).
 // At most S experts have rows.  All of them counted / those, 7168 values of k: 8 rows
 // over 64 experts x 2048 29.9 / 25.9, 8 over 16 x 4096 46.5 / 36.1, 3 over 8 x 4096
 // 30.7 / 24.6, 1 over 64 x 4096 27.2 / 23.0.
+// Sizes alone do not say how even the rows are, and the rule is not the best one
+// everywhere: 8 x 4096 x 7168, 96 even rows take 53 us where 128 x 128 takes 47; 4 x
+// 2048 x 4096, 256 even rows 30 where 64 x 128 takes 20; 1 x 4096 x 4096, 2048 rows 47
+// where 128 x 256 takes 41.
 // N: rows of one expert's weights (2 I when gated).
 inline GemmKernel choose_gemm(int64_t S, int64_t N, int64_t E, bool gated, int64_t cus)
 {
@@ -75,8 +81,9 @@ inline int64_t wgrad_tiles(int N, int K, int E, int tile)
 }
 
 // Large tiles want a whole round of them and rows enough to hide their stores
-// (16 experts x 2816 x 4096, large / small tiles: 128 rows each 145 / 133 us, 176
-// rows 170 / 170, 256 rows 169 / 186; 8 experts x 1024 x 1024, half a round: 35 / 31).
+// (16 experts x 2816 x 4096, large / small tiles: 128 rows each 134 / 122 us, 176
+// rows 150 / 139, 256 rows 155 / 163; 8 experts x 1024 x 1024, half a round: 256 rows
+// 14.5 / 13.0, but 4096 rows 85 / 100).
 inline bool wgrad_large(int S, int N, int K, int E)
 {
     return wgrad_tiles(N, K, E, kWgradTile) >= 256 && S >= int64_t(192) * E;
@@ -84,8 +91,8 @@ inline bool wgrad_large(int S, int N, int K, int E)
 
 // Parts that an expert's rows are split into: 1, unless there are few small
 // tiles (up to 192, towards 768 workgroups) and rows for several parts of 128.
-// 32768 rows, 256 x 512 (8 tiles): 372 us whole, 37 in 64 parts; 4 experts of 4096
-// rows, 512 x 512 (64 tiles): 54, 29 in 12; 8 of 4096, 512 x 1024 (256): 61, 70 in 3.
+// 32768 rows, 256 x 512 (8 tiles): 390 us whole, 35 in 64 parts; 4 experts of 4096
+// rows, 512 x 512 (64 tiles): 52, 27 in 12; 8 of 4096, 512 x 1024 (256): 57, 69 in 3.
 // From sizes alone, so that a workspace's size holds on every device.
 inline int wgrad_parts(int S, int N, int K, int E)
 {

@@ -17,9 +17,10 @@
 // tiles, so that the first loads of a tile and the stores of the one before it
 // hide behind matrix work.
 //
-// Measured on MI355X, 8 experts, sustained: 32768 rows x 7168 x 4096 in 802 to 820
-// us, 32768 x 4096 x 7168 in 765 to 811 (2.35 to 2.5 PFLOP/s; a library product of
-// one matrix of that size 656 to 692 and 611), the same gated 744.  The steps
+// Measured on MI355X, 8 experts, sustained: 32768 rows x 7168 x 4096 in 802 to 840
+// us, 32768 x 4096 x 7168 in 765 to 811 (2.3 to 2.5 PFLOP/s; a library product of
+// one matrix of that size 656 to 692 and 611), the same gated 744 to 753, with the
+// gate and up values kept 837.  The steps
 // before, at the first size: eight waves of 128 x 64 on two stages 1062; four
 // waves, 64 bytes of k on four stages, all loads of a step at once 990 (rows of 64
 // bytes ask the L2 for half lines); whole lines on two stages with one load after

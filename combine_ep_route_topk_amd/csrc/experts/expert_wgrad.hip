@@ -90,9 +90,10 @@ __device__ __forceinline__ void put_fragments(__amdgpu_buffer_rsrc_t r, uint8_t*
 // all waves meet: this step's stages have been read, the next step's have
 // landed.  The stream runs on across tiles.
 //
-// Measured on MI355X, 8 experts x 4096 x 7168, 4096 rows each: 1507 to 1550 us (1.26
+// Measured on MI355X, 8 experts x 4096 x 7168, 4096 rows each: 1492 to 1565 us (1.26
 // PFLOP/s; a library product of one matrix of that size with the same transposed
-// operands 1974 to 2035, with both turned beforehand 1530 to 1600); eight waves of 128 x 64 on two stages,
+// operands 1974 to 2035, with both turned beforehand 1530 to 1600), added to what is
+// there 1600 to 1608 (0.94 GB more are read); eight waves of 128 x 64 on two stages,
 // without the units' exchange, 3721 us, all of it LDS bank conflicts.
 //
 // LDS image of a stage: rows of 512 bytes in units of 64, unit u of row r at
@@ -306,8 +307,9 @@ __global__ __launch_bounds__(256, 1) void expert_wgrad_large_kernel(WgradArgs p)
 // ------------------------------------------------------------- small tiles
 // 128 i x 128 j, four waves of 64 x 64, steps of 32 rows on three stages (48 KB:
 // three workgroups a CU, one's stores behind another's loads).  Bound by what it
-// writes: 16 experts x 2816 x 4096 from 2000 ragged rows in 128 us, 6.0 TB/s; tiles
-// of a row of the output run together (column by column: 64 rows each 149 us, 133).  With few tiles
+// writes: 16 experts x 2816 x 4096 from 2000 ragged rows in 128 us, 6.0 TB/s (added
+// to what is there, 128 rows each, 244 us, 6.1 TB/s both ways); tiles of a row of the
+// output run together (column by column: 64 rows each 149 us, 133).  With few tiles
 // each expert's rows are split over `parts` workgroups a tile, whose sums go to
 // a workspace [part][E][N][K] and are joined in order by a second launch.
 constexpr int kSmallTile = kWgradSmallTile, kSmallRows = 32;

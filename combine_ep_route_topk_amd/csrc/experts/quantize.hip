@@ -5,9 +5,10 @@
 // max|x| / s <= 448 over the block.  Reading is one pass: a block's 128 values
 // sit in 8 lanes of one wave, its maximum takes three lane exchanges, and the
 // quantised values go straight to the rows' final places -- for ep_dispatch_fp8
-// to each of the token's k rows of the expert-contiguous buffer.  HBM-bound, most
-// of it writes: 4096 tokens of 7168 to 8 rows each in 48 us on MI355X, 6.1 TB/s; 64
-// tokens in 4 us, one round of latency.
+// to each of the token's k rows of the expert-contiguous buffer.  HBM-bound, for
+// a dispatch most of it writes: 4096 tokens of 7168 to 8 rows each in 48 us on MI355X,
+// 6.1 TB/s; 128 tokens in 4 us, one round of latency; 32768 rows as they are in 128 us,
+// 5.5 TB/s.
 #include "experts_internal.h"
 
 namespace ep {
@@ -116,7 +117,10 @@ hipError_t launch_rows(const uint16_t* x, int T, int H, int k, const int32_t* po
 }
 
 // One workgroup per 128 x 128 block: 16-value runs, 8 to a row, 4 to a thread.
-// The transposed copy goes through LDS (rows padded to 132 bytes).
+// The transposed copy goes through LDS (rows padded to 132 bytes).  A block's rows
+// are 256 bytes read and 128 written, and a workgroup waits for its maximum before it
+// writes: 8 experts x 4096 x 7168 in 132 us on MI355X, 5.4 TB/s; with the transposed
+// copy 178 us, 5.3 TB/s.
 __global__ __launch_bounds__(kBlock) void quantize_weight_kernel(
     const uint16_t* __restrict__ w, int N, int K, uint8_t* __restrict__ q,
     uint8_t* __restrict__ scale, uint8_t* __restrict__ q_t, uint8_t* __restrict__ scale_t)
