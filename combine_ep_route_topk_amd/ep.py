@@ -7,11 +7,12 @@ mirror the C entry points of the same name; outputs may be passed in
 pre-allocated (the benchmark does) or are allocated here with torch.empty.
 
 `stream` (a torch stream or a raw handle; default: the current one) is the
-stream that a call's kernels run on.  As in a `with torch.cuda.stream(stream)`
-block, what a call allocates belongs to that stream, and the caller orders the
-rest: tensors passed in are ready on it, and they, like results used
-on other streams, are not dropped before the work that uses them is done
-(Tensor.record_stream, or a wait).
+stream that a call's kernels run on.  What a call allocates belongs to that
+stream, and its outputs, once dropped, also wait for the work of the stream that
+was current at the call.  The caller orders the rest: tensors passed in are ready
+on `stream` and kept until the call is done, the current stream waits for it
+before it uses the results, and a third stream that uses them is named to the
+allocator (Tensor.record_stream).
 
 Importing this module loads the built library and fails loudly if it is
 missing: there is no CPU fallback.
@@ -150,14 +151,37 @@ def _on(stream, dev):
             else torch.cuda.stream(_stream_object(stream, dev)))
 
 
-def _empty(shape, dtype: torch.dtype, dev, stream) -> torch.Tensor:
-    """An output or a workspace made inside a call, from the memory of the stream that the call runs
-    on.  From another stream's, the block may be one that work pending there still uses, and the
-    allocator would hand it out there again, once it is dropped, while the call still runs."""
+def _scratch(shape, dtype: torch.dtype, dev, stream) -> torch.Tensor:
+    """Memory made inside a call, of the stream that the call runs on.  From another stream's, the
+    block may be one that work pending there still uses, and the allocator would hand it out there
+    again, once it is dropped, while the call still runs."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     with _on(stream, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _for_caller(t: torch.Tensor | None, dev, stream) -> None:
+    """An output of a call on another stream: dropped, it waits for the work of the current stream,
+    where the caller uses it, before the call's stream has its memory again."""
+    if t is not None and stream is not None:
+        t.record_stream(torch.cuda.current_stream(dev))
+
+
+def _empty(shape, dtype: torch.dtype, dev, stream) -> torch.Tensor:
+    """An output made inside a call."""
+    t = _scratch(shape, dtype, dev, stream)
+    _for_caller(t, dev, stream)
+    return t
+
+
+def _outputs(make, dev, stream) -> dict:
+    """The dict of outputs that `make` allocates (and initialises), inside a call."""
+    with _on(stream, dev):
+        out = make()
+    for t in out.values():
+        _for_caller(t, dev, stream)
+    return out
 
 
 def _ptr(t: torch.Tensor | None):
@@ -228,8 +252,7 @@ def ep_dispatch_layout(topk_idx: torch.Tensor, E: int, R: int, out: dict | None 
     T, k = topk_idx.shape
     dev = topk_idx.device
     if out is None:
-        with _on(stream, dev):
-            out = layout_outputs(T, k, E, R, dev)
+        out = _outputs(lambda: layout_outputs(T, k, E, R, dev), dev, stream)
     ws = out["workspace"]
     _need(ws, "workspace", torch.uint8)
     for name, shape in (("expert_counts", (E,)), ("expert_offsets", (E + 1,)),
@@ -387,8 +410,7 @@ def ep_fused_dispatch_combine(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: t
     k = topk_idx.shape[1]
     _need(topk_w, "topk_w", torch.float32, (T, k))
     if out is None:
-        with _on(stream, x.device):      # the workspace's initialisation with it
-            out = fused_outputs(T, H, k, E, R, x.device)
+        out = _outputs(lambda: fused_outputs(T, H, k, E, R, x.device), x.device, stream)
     st = _stream(stream, x.device)
     if sync == EP_FUSED_SYNC_ITEM_EVENTS and not spin_limit:
         _check(_lib.ep_fused_dispatch_combine(
@@ -465,8 +487,7 @@ def ep_rank_coalesce(topk_idx: torch.Tensor, E: int, R: int, out: dict | None = 
     T, k = topk_idx.shape
     dev = topk_idx.device
     if out is None:
-        with _on(stream, dev):
-            out = coalesce_outputs(T, k, E, R, dev)
+        out = _outputs(lambda: coalesce_outputs(T, k, E, R, dev), dev, stream)
     ws = out["workspace"]
     _need(ws, "workspace", torch.uint8)
     for name, shape in (("rank_counts", (R,)), ("rank_offsets", (R + 1,)),
@@ -786,7 +807,7 @@ def ep_expert_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch
     if workspace is None:
         need = ep_expert_wgrad_workspace_bytes(S, N, K, E)
         if need:
-            workspace = _empty(need, torch.uint8, dev, stream)
+            workspace = _scratch(need, torch.uint8, dev, stream)
     if workspace is not None:
         _need(workspace, "workspace", torch.uint8)
     _launch(_lib.ep_expert_wgrad, dev, stream, (x, expert_offsets, grad_w, workspace),
@@ -829,7 +850,7 @@ def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     if out is None:
         out = _empty((T, H), x.dtype, dev, stream)
     if workspace is None:
-        workspace = _empty(ep_moe_tokens_workspace_bytes(T, k, I), torch.uint8, dev, stream)
+        workspace = _scratch(ep_moe_tokens_workspace_bytes(T, k, I), torch.uint8, dev, stream)
     _bits_ok(out, "out", (T, H))
     _need(workspace, "workspace", torch.uint8)
     _launch(_lib.ep_moe_tokens, dev, stream,

@@ -141,3 +141,50 @@ def test_pending_work_of_the_current_stream(ep, name):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("name", ["gemm", "moe_tokens", "swiglu_grad", "quantize", "layout", "dispatch", "fused",
+                                  "combine"])
+def test_dropped_outputs_wait_for_their_reader(ep, name):
+    """Results read by work that is pending on the current stream and dropped: the call's stream does not
+    get their memory before that work is done."""
+    call = calls(ep)[name]
+    want = [t.clone() for t in known(call(None))]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    say(f"{name} dropped beside pending reads")
+    got = call(s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(20_000_000)
+    mine = [t.clone() for t in known(got)]
+    sizes = [t.numel() * t.element_size() for t in tensors(got)]
+    del got
+    with torch.cuda.stream(s):
+        blocks = [torch.full((n,), 0x5A, dtype=torch.uint8, device=DEV) for n in sizes]
+    torch.cuda.synchronize()
+    for a, b in zip(mine, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+    del blocks
+
+
+@pytest.mark.parametrize("name", ["gemm", "moe_tokens", "wgrad_parts", "layout"])
+def test_captured_on_a_forked_stream(ep, name):
+    """A call on a stream that a capture forked to: replays equal the eager results."""
+    call = calls(ep)[name]
+    want = [t.clone() for t in known(call(None))]
+    torch.cuda.synchronize()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    say(f"{name} captured on a forked stream")
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = call(s)
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(3):
+        for t in known(got):
+            t.view(torch.uint8).fill_(0x5A)
+        call(None)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(known(got), want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
