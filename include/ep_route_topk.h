@@ -522,7 +522,8 @@ ep_status ep_exchange_waves(int32_t N, int32_t* peer);
  *   send e4m3 [T*k][H] out   scale u8 [T*k][ceil(H/128)] out.
  * ep_quantize_weight_fp8: weights, and with q_t and scale_t (both or neither)
  * also the transposed matrices, the same values: what the input gradient
- * multiplies by.
+ * multiplies by.  N is the rows of the call: gate and up rows of I > 2^16 are
+ * quantised apart (whole blocks), as the gated products take I up to 2^17.
  *   w bf16 [E][N][K]   q e4m3 [E][N][K] out   scale u8 [E][ceil(N/128)][ceil(K/128)] out
  *   q_t e4m3 [E][K][N] out   scale_t u8 [E][ceil(K/128)][ceil(N/128)] out.
  * ------------------------------------------------------------------------- */
