@@ -231,16 +231,6 @@ __global__ __launch_bounds__(WAVES* kWave) void expert_gemm_stream_kernel(GemmAr
     }
 }
 
-// Tiles of TM rows x TN weight rows (a multiple of 8, for the XCDs), 0 when a
-// launch cannot hold them; sets p.max_tiles.
-uint32_t gemm_tiles(GemmArgs& p, int TM, int TN)
-{
-    const int64_t mt = p.S / TM + (p.E < p.S ? p.E : p.S);
-    p.max_tiles = int(mt);
-    const int64_t grid = (mt * ((p.N + TN - 1) / TN) + 7) / 8 * 8;
-    return grid < (int64_t(1) << 30) ? uint32_t(grid) : 0;
-}
-
 template <int TM, int WAVES, int ROWS, bool GATED>
 hipError_t launch_stream(GemmArgs p, hipStream_t s)
 {

@@ -31,7 +31,7 @@
 // third step waits for the last tile's stores.
 #pragma once
 
-#include "experts_internal.h"
+#include "expert_tiles.h"
 
 namespace ep {
 namespace {
@@ -47,62 +47,6 @@ struct GemmArgs {
     uint16_t* y;         // plain: [S][N]; gated: gate_up [S][N] or NULL
     uint8_t* h;          // gated: [S][N/2]
     uint8_t* h_scale;    // gated: [S][N/256]
-};
-
-// Order of the tiles.  The 8 XCDs take contiguous shares of them (workgroups go
-// to the XCDs in turn); within a share, groups of 8 row tiles x all n tiles, row
-// tiles fastest: the 32 workgroups that an XCD runs at once read 8 row tiles and
-// 4 weight tiles through its L2.
-struct GemmTile {
-    RowTile rows;    // rows.expert = -1: none
-    int n;           // n tile
-};
-struct GemmTiles {
-    int mt, nt;          // row tiles, n tiles
-    int b, end, upto;    // up to 64 experts: lane's segment, and the tiles up to its end
-
-    __device__ __forceinline__ GemmTiles(const GemmArgs& p, int TM, int n_tiles) : nt(n_tiles) {
-        b = end = upto = 0;
-        if (p.E <= kWave) {
-            if (lane_id() < p.E) segment_of(p.offsets, lane_id(), p.S, b, end);
-            int tiles = (end - b + TM - 1) / TM;
-            tiles = tiles < (1 << 24) ? tiles : (1 << 24);
-            upto = wave_inclusive_sum(tiles);
-            mt = __builtin_amdgcn_readlane(upto, kWave - 1);
-            mt = mt < p.max_tiles ? mt : p.max_tiles;
-        } else {
-            mt = count_row_tiles(p.offsets, p.E, p.S, TM, p.max_tiles);
-        }
-    }
-    // The workgroup's tile number `turn`, of those of its XCD slot / 8 apart by
-    // gridDim / 8.
-    __device__ __forceinline__ GemmTile at(const GemmArgs& p, int TM, int turn) const {
-        GemmTile t;
-        t.rows = RowTile{-1, 0, 0};
-        t.n = 0;
-        const int total = mt * nt, per = (total + 7) / 8;
-        const int in_share = int(blockIdx.x / 8) + turn * int(gridDim.x / 8);
-        const int id = int(blockIdx.x % 8) * per + in_share;
-        if (in_share >= per || id >= total) return t;
-        constexpr int kGroup = 8;
-        const int group = id / (kGroup * nt);
-        const int gsize = mt - group * kGroup < kGroup ? mt - group * kGroup : kGroup;
-        const int in = id - group * kGroup * nt;
-        t.n = in / gsize;
-        const int index = group * kGroup + in % gsize;
-        if (p.E > kWave) {
-            t.rows = find_row_tile(p.offsets, p.E, p.S, TM, index);
-            return t;
-        }
-        const uint64_t past = ballot(upto > index);
-        if (!past) return t;
-        const int l = __builtin_ctzll(past);
-        const int before = l ? __builtin_amdgcn_readlane(upto, l - 1) : 0;
-        t.rows.expert = l;
-        t.rows.row0 = __builtin_amdgcn_readlane(b, l) + (index - before) * TM;
-        t.rows.end = __builtin_amdgcn_readlane(end, l);
-        return t;
-    }
 };
 
 constexpr int kLargeTile = 256;

@@ -52,6 +52,14 @@ ep_status check_quantize(const char* fn, int32_t T, int32_t H, int32_t k)
     return EP_OK;
 }
 
+// A sum of K products of two 8-bit integers stays below 2^31.
+ep_status check_int8_sum(const char* fn, int32_t K)
+{
+    if (K >= (1 << 17))
+        return fail(EP_ERR_UNSUPPORTED, "%s: K=%d must be < 2^17 in 8-bit integers", fn, K);
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -199,6 +207,130 @@ ep_status ep_swiglu_grad(const uint16_t* grad_h, const uint16_t* gate_up, int32_
     return launched(ep::launch_swiglu_grad(grad_h, gate_up, S, I, grad_gate_up, h,
                                            static_cast<hipStream_t>(stream)),
                     fn);
+}
+
+ep_status ep_expert_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* expert_offsets,
+                              int32_t S, int32_t N, int32_t K, int32_t E, int32_t transposed,
+                              uint16_t* y, void* stream)
+{
+    const char* fn = "ep_expert_gemm_bf16";
+    TimingScope timing_scope;
+    EP_TRY(check_expert_sizes(fn, S, N, K, E, 8, "N", "K"));
+    if (S == 0) return ok();
+    EP_REQUIRE_PTR(fn, a, 16);
+    EP_REQUIRE_PTR(fn, w, 16);
+    EP_REQUIRE_PTR(fn, expert_offsets, 4);
+    EP_REQUIRE_PTR(fn, y, 16);
+    return launched(ep::launch_expert_gemm_bf16(a, w, expert_offsets, S, N, K, E, transposed != 0, y,
+                                                static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+ep_status ep_expert_swiglu_bf16(const uint16_t* a, const uint16_t* w13, const int32_t* expert_offsets,
+                                int32_t S, int32_t I, int32_t K, int32_t E, uint16_t* h,
+                                uint16_t* gate_up, void* stream)
+{
+    const char* fn = "ep_expert_swiglu_bf16";
+    TimingScope timing_scope;
+    EP_TRY(check_expert_sizes(fn, S, I, K, E, 8, "I", "K"));
+    if (S == 0) return ok();
+    EP_REQUIRE_PTR(fn, a, 16);
+    EP_REQUIRE_PTR(fn, w13, 16);
+    EP_REQUIRE_PTR(fn, expert_offsets, 4);
+    EP_REQUIRE_PTR(fn, h, 16);
+    EP_REQUIRE_ALIGNED(fn, gate_up, 16);
+    return launched(ep::launch_expert_swiglu_bf16(a, w13, expert_offsets, S, I, K, E, h, gate_up,
+                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+ep_status ep_quantize_int8(const uint16_t* x, int32_t S, int32_t H, int8_t* q, float* scale,
+                           void* stream)
+{
+    const char* fn = "ep_quantize_int8";
+    TimingScope timing_scope;
+    if (S < 0) return fail(EP_ERR_INVALID_ARG, "%s: S=%d must be >= 0", fn, S);
+    EP_TRY(check_quantize(fn, S, H, 1));
+    if (S == 0) return ok();
+    EP_REQUIRE_PTR(fn, x, 16);
+    EP_REQUIRE_PTR(fn, q, 16);
+    EP_REQUIRE_PTR(fn, scale, 4);
+    return launched(ep::launch_quantize_rows_int8(x, S, H, 1, nullptr, nullptr, nullptr, q, scale,
+                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+ep_status ep_dispatch_int8(const uint16_t* x, int32_t T, int32_t H, int32_t k, const int32_t* pos,
+                           int8_t* send, float* scale, void* stream)
+{
+    const char* fn = "ep_dispatch_int8";
+    TimingScope timing_scope;
+    if (T < 1) return fail(EP_ERR_INVALID_ARG, "%s: T=%d must be >= 1", fn, T);
+    EP_TRY(check_quantize(fn, T, H, k));
+    EP_REQUIRE_PTR(fn, x, 16);
+    EP_REQUIRE_PTR(fn, pos, 4);
+    EP_REQUIRE_PTR(fn, send, 16);
+    EP_REQUIRE_PTR(fn, scale, 4);
+    return launched(ep::launch_quantize_rows_int8(x, T, H, k, pos, nullptr, nullptr, send, scale,
+                                                  static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+ep_status ep_expert_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w,
+                              const float* w_scale, const int32_t* expert_offsets, int32_t S,
+                              int32_t N, int32_t K, int32_t E, uint16_t* y, void* stream)
+{
+    const char* fn = "ep_expert_gemm_int8";
+    TimingScope timing_scope;
+    EP_TRY(check_expert_sizes(fn, S, N, K, E, 16, "N", "K"));
+    EP_TRY(check_int8_sum(fn, K));
+    if (S == 0) return ok();
+    EP_REQUIRE_PTR(fn, a, 16);
+    EP_REQUIRE_PTR(fn, a_scale, 4);
+    EP_REQUIRE_PTR(fn, w, 16);
+    EP_REQUIRE_PTR(fn, w_scale, 16);
+    EP_REQUIRE_PTR(fn, expert_offsets, 4);
+    EP_REQUIRE_PTR(fn, y, 16);
+    return launched(ep::launch_expert_gemm_int8(a, a_scale, w, w_scale, expert_offsets, S, N, K, E, y,
+                                                static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+size_t ep_expert_swiglu_int8_workspace_bytes(int32_t S, int32_t I)
+{
+    return S < 1 || I < 1 ? 0 : size_t(S) * I * sizeof(uint16_t);
+}
+
+ep_status ep_expert_swiglu_int8(const int8_t* a, const float* a_scale, const int8_t* w13,
+                                const float* w13_scale, const int32_t* expert_offsets, int32_t S,
+                                int32_t I, int32_t K, int32_t E, int8_t* h, float* h_scale,
+                                void* workspace, size_t workspace_bytes, void* stream)
+{
+    const char* fn = "ep_expert_swiglu_int8";
+    TimingScope timing_scope;
+    EP_TRY(check_expert_sizes(fn, S, I, K, E, 16, "I", "K"));
+    EP_TRY(check_int8_sum(fn, K));
+    if (S == 0) return ok();
+    EP_REQUIRE_PTR(fn, a, 16);
+    EP_REQUIRE_PTR(fn, a_scale, 4);
+    EP_REQUIRE_PTR(fn, w13, 16);
+    EP_REQUIRE_PTR(fn, w13_scale, 16);
+    EP_REQUIRE_PTR(fn, expert_offsets, 4);
+    EP_REQUIRE_PTR(fn, h, 16);
+    EP_REQUIRE_PTR(fn, h_scale, 4);
+    EP_REQUIRE_PTR(fn, workspace, 256);
+    const size_t need = ep_expert_swiglu_int8_workspace_bytes(S, I);
+    if (workspace_bytes < need)
+        return fail(EP_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes,
+                    need);
+    uint16_t* const rows = static_cast<uint16_t*>(workspace);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = ep::launch_expert_swiglu_int8(a, a_scale, w13, w13_scale, expert_offsets, S, I, K, E,
+                                                 rows, s);
+    if (e == hipSuccess)
+        e = ep::launch_quantize_rows_int8(rows, S, I, 1, nullptr, expert_offsets, expert_offsets + E, h,
+                                          h_scale, s);
+    return launched(e, fn);
 }
 
 size_t ep_moe_tokens_workspace_bytes(int32_t T, int32_t k, int32_t I)

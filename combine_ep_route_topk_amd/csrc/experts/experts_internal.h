@@ -42,6 +42,23 @@ hipError_t launch_moe_tokens(const uint16_t* x, const int32_t* idx, const float*
                              const void* w2, const uint8_t* w2_scale, uint16_t* out, void* ws,
                              hipStream_t s);
 
+hipError_t launch_expert_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* offsets,
+                                   int S, int N, int K, int E, bool transposed, uint16_t* y,
+                                   hipStream_t s);
+hipError_t launch_expert_swiglu_bf16(const uint16_t* a, const uint16_t* w13, const int32_t* offsets,
+                                     int S, int I, int K, int E, uint16_t* h, uint16_t* gate_up,
+                                     hipStream_t s);
+// `first` and `past` (both or neither): only the rows [*first, *past).
+hipError_t launch_quantize_rows_int8(const uint16_t* x, int T, int H, int k, const int32_t* pos,
+                                     const int32_t* first, const int32_t* past, int8_t* q,
+                                     float* scale, hipStream_t s);
+hipError_t launch_expert_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w,
+                                   const float* w_scale, const int32_t* offsets, int S, int N, int K,
+                                   int E, uint16_t* y, hipStream_t s);
+hipError_t launch_expert_swiglu_int8(const int8_t* a, const float* a_scale, const int8_t* w13,
+                                     const float* w13_scale, const int32_t* offsets, int S, int I,
+                                     int K, int E, uint16_t* h, hipStream_t s);
+
 // ----------------------------------------------------------------- device
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));

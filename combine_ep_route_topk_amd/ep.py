@@ -86,6 +86,14 @@ _SIGS = {
     "ep_swiglu_grad": ([_P, _P, _i32, _i32, _P, _P, _P], ctypes.c_int),
     "ep_expert_wgrad_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
     "ep_expert_wgrad": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P, _sz, _P], ctypes.c_int),
+    "ep_expert_gemm_bf16": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P], ctypes.c_int),
+    "ep_expert_swiglu_bf16": ([_P, _P, _P, _i32, _i32, _i32, _i32, _P, _P, _P], ctypes.c_int),
+    "ep_quantize_int8": ([_P, _i32, _i32, _P, _P, _P], ctypes.c_int),
+    "ep_dispatch_int8": ([_P, _i32, _i32, _i32, _P, _P, _P, _P], ctypes.c_int),
+    "ep_expert_gemm_int8": ([_P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P], ctypes.c_int),
+    "ep_expert_swiglu_int8_workspace_bytes": ([_i32, _i32], _sz),
+    "ep_expert_swiglu_int8": ([_P, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P, _P, _sz, _P],
+                              ctypes.c_int),
     "ep_moe_tokens_workspace_bytes": ([_i32, _i32, _i32], _sz),
     "ep_moe_tokens": ([_P, _P, _P, _i32, _i32, _i32, _i32, _i32, _P, _P, _P, _P, _P, _P, _sz, _P],
                       ctypes.c_int),
@@ -814,6 +822,159 @@ def ep_expert_wgrad(grad_y: torch.Tensor, x: torch.Tensor, expert_offsets: torch
             _ptr(grad_y), _ptr(x), _ptr(expert_offsets), S, N, K, E, int(bool(accumulate)),
             _ptr(grad_w), _ptr(workspace), workspace.numel() if workspace is not None else 0)
     return grad_w
+
+
+def ep_expert_gemm_bf16(a: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor,
+                        transposed: bool = False, y: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """a bf16 [S][K], w bf16 [E][N][K], expert_offsets i32 [E+1] -> y bf16 [S][N], y[s] = W[e(s)] a[s].
+    `transposed`: w bf16 [E][K][N], y[s] = W[e(s)]^T a[s], the input gradient from the forward
+    weights."""
+    S, K = _shape(a, "a", 2)
+    _bits_ok(a, "a")
+    E, rows, cols = _shape(w, "w", 3)
+    N = cols if transposed else rows
+    _bits_ok(w, "w", (E, K, N) if transposed else (E, N, K))
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    dev = a.device
+    if y is None:
+        y = _empty((S, N), a.dtype, dev, stream)
+    else:
+        _bits_ok(y, "y", (S, N))
+    _launch(_lib.ep_expert_gemm_bf16, dev, stream, (w, expert_offsets, y), _ptr(a), _ptr(w),
+            _ptr(expert_offsets), S, N, K, E, int(bool(transposed)), _ptr(y))
+    return y
+
+
+def ep_expert_swiglu_bf16(a: torch.Tensor, w13: torch.Tensor, expert_offsets: torch.Tensor,
+                          h: torch.Tensor | None = None, gate_up: torch.Tensor | None = None,
+                          save_gate_up: bool = False, stream=None):
+    """a bf16 [S][K], w13 bf16 [E][2I][K] (gate rows, then up rows) -> (h bf16 [S][I], gate_up bf16
+    [S][2I] or None): h = silu(g) * u.  gate_up is written when it is passed in or save_gate_up is
+    true."""
+    S, K = _shape(a, "a", 2)
+    _bits_ok(a, "a")
+    E, N, _ = _shape(w13, "w13", 3)
+    _bits_ok(w13, "w13", (E, N, K))
+    if N % 2:
+        raise ValueError("w13 must hold as many gate rows as up rows")
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    dev, I = a.device, N // 2
+    if h is None:
+        h = _empty((S, I), a.dtype, dev, stream)
+    else:
+        _bits_ok(h, "h", (S, I))
+    if gate_up is None and save_gate_up:
+        gate_up = _empty((S, N), a.dtype, dev, stream)
+    elif gate_up is not None:
+        _bits_ok(gate_up, "gate_up", (S, N))
+    _launch(_lib.ep_expert_swiglu_bf16, dev, stream, (w13, expert_offsets, h, gate_up), _ptr(a),
+            _ptr(w13), _ptr(expert_offsets), S, I, K, E, _ptr(h), _ptr(gate_up))
+    return h, gate_up
+
+
+def ep_quantize_int8(x: torch.Tensor, q: torch.Tensor | None = None,
+                     scale: torch.Tensor | None = None, stream=None):
+    """x bf16 [..., H] -> (q i8 [..., H], scale f32 [...]): rows of tokens [S][H], or the channels of
+    weights [E][N][K]."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.dim() < 2:
+        raise ValueError(f"x must have 2 dimensions or more, got {x.dim()}")
+    _bits_ok(x, "x")
+    dev, rows, H = x.device, x.shape[:-1], x.shape[-1]
+    if q is None:
+        q = _empty(x.shape, torch.int8, dev, stream)
+    else:
+        _need(q, "q", torch.int8, x.shape)
+    if scale is None:
+        scale = _empty(rows, torch.float32, dev, stream)
+    else:
+        _need(scale, "scale", torch.float32, rows)
+    _launch(_lib.ep_quantize_int8, dev, stream, (q, scale), _ptr(x), rows.numel(), H, _ptr(q),
+            _ptr(scale))
+    return q, scale
+
+
+def ep_dispatch_int8(x: torch.Tensor, pos: torch.Tensor, send: torch.Tensor | None = None,
+                     scale: torch.Tensor | None = None, stream=None):
+    """x bf16 [T][H], pos i32 [T][k] -> (send i8 [T*k][H], scale f32 [T*k])."""
+    T, H = _shape(x, "x", 2)
+    _bits_ok(x, "x")
+    k = _shape(pos, "pos", 2)[1]
+    _need(pos, "pos", torch.int32, (T, k))
+    dev = x.device
+    if send is None:
+        send = _empty((T * k, H), torch.int8, dev, stream)
+    else:
+        _need(send, "send", torch.int8, (T * k, H))
+    if scale is None:
+        scale = _empty((T * k,), torch.float32, dev, stream)
+    else:
+        _need(scale, "scale", torch.float32, (T * k,))
+    _launch(_lib.ep_dispatch_int8, dev, stream, (pos, send, scale), _ptr(x), T, H, k, _ptr(pos),
+            _ptr(send), _ptr(scale))
+    return send, scale
+
+
+def _int8_operands(a, a_scale, w, w_scale, expert_offsets, w_name):
+    S, K = _shape(a, "a", 2)
+    _need(a, "a", torch.int8)
+    _need(a_scale, "a_scale", torch.float32, (S,))
+    E, N, _ = _shape(w, w_name, 3)
+    _need(w, w_name, torch.int8, (E, N, K))
+    _need(w_scale, w_name + "_scale", torch.float32, (E, N))
+    _need(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    return S, N, K, E
+
+
+def ep_expert_gemm_int8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor,
+                        w_scale: torch.Tensor, expert_offsets: torch.Tensor,
+                        y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """a i8 [S][K] with a_scale f32 [S], w i8 [E][N][K] with w_scale f32 [E][N], expert_offsets i32
+    [E+1] -> y bf16 [S][N], y[s][n] = a_scale[s] w_scale[e][n] sum_k a[s][k] W[e][n][k]."""
+    S, N, K, E = _int8_operands(a, a_scale, w, w_scale, expert_offsets, "w")
+    dev = a.device
+    if y is None:
+        y = _empty((S, N), torch.bfloat16, dev, stream)
+    else:
+        _bits_ok(y, "y", (S, N))
+    _launch(_lib.ep_expert_gemm_int8, dev, stream, (a_scale, w, w_scale, expert_offsets, y),
+            _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(expert_offsets), S, N, K, E, _ptr(y))
+    return y
+
+
+def ep_expert_swiglu_int8_workspace_bytes(S: int, I: int) -> int:
+    return int(_lib.ep_expert_swiglu_int8_workspace_bytes(S, I))
+
+
+def ep_expert_swiglu_int8(a: torch.Tensor, a_scale: torch.Tensor, w13: torch.Tensor,
+                          w13_scale: torch.Tensor, expert_offsets: torch.Tensor,
+                          h: torch.Tensor | None = None, h_scale: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """a i8 [S][K] with a_scale, w13 i8 [E][2I][K] (gate rows, then up rows) with w13_scale f32 [E][2I]
+    -> (h i8 [S][I], h_scale f32 [S]): silu(g) * u, rounded to bf16 and quantised row by row.  Calls
+    that overlap need a `workspace` each (by default every call gets its own)."""
+    S, N, K, E = _int8_operands(a, a_scale, w13, w13_scale, expert_offsets, "w13")
+    if N % 2:
+        raise ValueError("w13 must hold as many gate rows as up rows")
+    dev, I = a.device, N // 2
+    if h is None:
+        h = _empty((S, I), torch.int8, dev, stream)
+    else:
+        _need(h, "h", torch.int8, (S, I))
+    if h_scale is None:
+        h_scale = _empty((S,), torch.float32, dev, stream)
+    else:
+        _need(h_scale, "h_scale", torch.float32, (S,))
+    if workspace is None:
+        workspace = _scratch(ep_expert_swiglu_int8_workspace_bytes(S, I), torch.uint8, dev, stream)
+    _need(workspace, "workspace", torch.uint8)
+    _launch(_lib.ep_expert_swiglu_int8, dev, stream,
+            (a_scale, w13, w13_scale, expert_offsets, h, h_scale, workspace),
+            _ptr(a), _ptr(a_scale), _ptr(w13), _ptr(w13_scale), _ptr(expert_offsets), S, I, K, E,
+            _ptr(h), _ptr(h_scale), _ptr(workspace), workspace.numel())
+    return h, h_scale
 
 
 def ep_moe_tokens_workspace_bytes(T: int, k: int, I: int) -> int:

@@ -597,6 +597,66 @@ ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32
                           float* grad_w, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The experts' products in bf16.  Sums are f32, rounded once to bf16 (nearest
+ * even); infinities and NaN go through.
+ *
+ * ep_expert_gemm_bf16: y[s] = W[e] a[s] for every row s of every expert e, or with
+ * transposed != 0 y[s] = W[e]^T a[s]: the input gradient from the forward weights
+ * as they lie (N is then their row length, K the number of rows).
+ *   a bf16 [S][K]   w bf16 [E][N][K], transposed [E][K][N]   y bf16 [S][N] out.
+ * ep_expert_swiglu_bf16: [g; u] = W13[e] a[s] (rows [0, I) of W13 the gate, [I, 2I)
+ * the up projection), h = silu(g) * u in f32, rounded once.
+ *   a bf16 [S][K]   w13 bf16 [E][2I][K]   h bf16 [S][I] out
+ *   gate_up bf16 [S][2I] out, or NULL: g and u rounded, for ep_swiglu_grad.
+ * With ep_swiglu_grad and ep_expert_wgrad they are a layer and its gradients.
+ * ------------------------------------------------------------------------- */
+ep_status ep_expert_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* expert_offsets,
+                              int32_t S, int32_t N, int32_t K, int32_t E, int32_t transposed,
+                              uint16_t* y, void* stream);
+ep_status ep_expert_swiglu_bf16(const uint16_t* a, const uint16_t* w13, const int32_t* expert_offsets,
+                                int32_t S, int32_t I, int32_t K, int32_t E, uint16_t* h,
+                                uint16_t* gate_up, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The same in 8-bit integers with one f32 scale for each row: a token's, or that
+ * of an output channel (a row of a weight matrix).
+ *
+ * The quantisers take m = max(max|x|, 127 * 2^-126) over the row: scale = m / 127
+ * in f32, q = 127 x / m rounded to the nearest integer, ties to even (exactly:
+ * -127 .. 127).  A row with an infinity or a NaN gets the scale NaN and zeros, so
+ * that its products are NaN.  H % 16 == 0.
+ * ep_quantize_int8: rows as they are; weights [E][N][K] are S = E N rows of K.
+ *   x bf16 [S][H]   q i8 [S][H] out   scale f32 [S] out.
+ * ep_dispatch_int8: ep_dispatch with the rows quantised on the way, each row once;
+ * pos entries outside [0, T*k) are skipped.  T >= 1.
+ *   send i8 [T*k][H] out   scale f32 [T*k] out.
+ *
+ * ep_expert_gemm_int8: y[s][n] = a_scale[s] (w_scale[e][n] sum_k a[s][k] W[e][n][k]),
+ * the sum in 32-bit integers, exact, then f32, rounded once to bf16.
+ *   a i8 [S][K], a_scale f32 [S]   w i8 [E][N][K], w_scale f32 [E][N], 16-byte aligned
+ *   y bf16 [S][N] out.  K < 2^17.
+ * ep_expert_swiglu_int8: the gated product as above, h rounded to bf16 and
+ * quantised as ep_quantize_int8 does: what ep_expert_gemm_int8 takes with the
+ * second weights.
+ *   w13 i8 [E][2I][K], w13_scale f32 [E][2I], 16-byte aligned; I % 16 == 0, K < 2^17
+ *   h i8 [S][I] out, h_scale f32 [S] out
+ *   workspace ep_expert_swiglu_int8_workspace_bytes(S, I) bytes, 256-byte aligned;
+ *   contents need no initialisation.  Calls that share one must not overlap.
+ * ------------------------------------------------------------------------- */
+ep_status ep_quantize_int8(const uint16_t* x, int32_t S, int32_t H, int8_t* q, float* scale,
+                           void* stream);
+ep_status ep_dispatch_int8(const uint16_t* x, int32_t T, int32_t H, int32_t k, const int32_t* pos,
+                           int8_t* send, float* scale, void* stream);
+ep_status ep_expert_gemm_int8(const int8_t* a, const float* a_scale, const int8_t* w,
+                              const float* w_scale, const int32_t* expert_offsets, int32_t S,
+                              int32_t N, int32_t K, int32_t E, uint16_t* y, void* stream);
+size_t ep_expert_swiglu_int8_workspace_bytes(int32_t S, int32_t I);
+ep_status ep_expert_swiglu_int8(const int8_t* a, const float* a_scale, const int8_t* w13,
+                                const float* w13_scale, const int32_t* expert_offsets, int32_t S,
+                                int32_t I, int32_t K, int32_t E, int8_t* h, float* h_scale,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * The whole layer for 1 <= T <= 64 tokens (one decoding step), in two launches:
  *   out[t] = sum_j topk_w[t][j] W2[e] (silu(g) * u), [g; u] = W13[e] x[t],
  *   e = topk_idx[t][j].
