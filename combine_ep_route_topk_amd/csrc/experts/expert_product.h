@@ -1,0 +1,415 @@
+// expert_product.h -- the grouped product's kernel for operands without block
+// scales: bf16, and 8-bit integers.
+//
+// For a row s of expert e:
+//   bf16:  y[s][n] = sum_k a[s][k] W[e][n][k]            (f32 sums, rounded once)
+//          y[s][n] = sum_k a[s][k] W[e][k][n]            (transposed)
+//   int8:  y[s][n] = as[s] (ws[e][n] sum_k a[s][k] W[e][n][k])   (integer sums)
+//   gated: g and u so from the rows [0, I) and [I, 2I) of W, h = silu(g) u in f32,
+//          rounded once to bf16.
+//
+// A persistent workgroup of four waves, WN of them along the weight rows, makes TN =
+// 32 FN WN weight rows x TM = 32 FM (4 / WN) tokens at a time with 32 x 32 matrix
+// instructions of 16 bytes of k a lane; the weights are the row operand, so a lane
+// holds four neighbouring n of one token.  A step is 128 bytes of k of every row:
+// whole lines from memory.  Its loads go straight into LDS, STAGES of the weights and
+// one less of the tokens, the stream running on across tiles, so that a tile's first
+// loads and the stores of the one before it hide behind matrix work.  A step's four
+// quarters work on fragments in registers while the next quarter's are read.
+// Before the last quarter all waves meet: this step's stages have been read, the
+// next step's have landed.  The weights of step s + STAGES - 1 are asked for in the
+// first half of step s, into the stage that step s - 1 left; the tokens of it in the
+// last quarter, into the stage that s itself has just left.
+#pragma once
+
+#include "expert_tiles.h"
+
+namespace ep {
+namespace {
+
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+struct ProductArgs {
+    const uint8_t* a;
+    const float* a_scale;
+    const uint8_t* w;
+    const float* w_scale;
+    const int32_t* offsets;
+    int S, N, K, E;      // N: columns of y, half the weights' rows when gated
+    int max_tiles;       // row tiles that S rows in E segments can make
+    uint16_t* y;         // plain: [S][N]; gated: gate_up [S][2N], if wanted
+    uint16_t* h;         // gated: [S][N]
+};
+
+struct Bf16 {
+    typedef f32x16 Acc;
+    static constexpr int kBytes = 2;
+    static constexpr bool kScaled = false;
+    static __device__ __forceinline__ Acc mfma(u32x4 w, u32x4 x, Acc c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w),
+                                                       __builtin_bit_cast(bf16x8, x), c, 0, 0, 0);
+    }
+};
+struct Int8 {
+    typedef i32x16 Acc;
+    static constexpr int kBytes = 1;
+    static constexpr bool kScaled = true;
+    static __device__ __forceinline__ Acc mfma(u32x4 w, u32x4 x, Acc c) {
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, w),
+                                                     __builtin_bit_cast(i32x4, x), c, 0, 0, 0);
+    }
+};
+
+enum ProductKind { kPlain, kTransposed, kGated, kGatedSaved };
+
+template <class T_, ProductKind KIND_, int FN_, int FM_, int WN_, int STAGES_, bool STREAM_>
+struct ProductShape {
+    typedef T_ T;
+    static constexpr ProductKind KIND = KIND_;
+    static constexpr int FN = FN_, FM = FM_, WN = WN_, STAGES = STAGES_;
+    static constexpr bool STREAM = STREAM_;      // the weights past the caches, k from a turn of its own
+    static constexpr bool TRANS = KIND == kTransposed, GATED = KIND >= kGated;
+    static constexpr int TN = 32 * FN * WN, TM = 32 * FM * (4 / WN);
+    static constexpr int kColumns = GATED ? TN / 2 : TN;      // of y or h
+    static constexpr int kLds = (STAGES * TN + (STAGES - 1) * TM) * 128;
+    static constexpr int kOccupancy = kLds > 80 * 1024 ? 1 : kLds > 160 * 1024 / 3 ? 2 : 3;
+    // stores of one tile that every wave issues
+    static constexpr int kStores = (KIND == kGated ? 1 : KIND == kGatedSaved ? 3 : 2) * FN * FM;
+    static constexpr bool kStoreNt = TN == 256 && TM == 256;
+    static_assert(!GATED || FN % 2 == 0, "gate and up rows alternate");
+    static_assert(!TRANS || TN >= 128, "a row of a transposed stage has four units at least");
+};
+
+template <class P>
+__global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(ProductArgs p)
+{
+    typedef typename P::T T;
+    constexpr int FN = P::FN, FM = P::FM, TN = P::TN, TM = P::TM, STAGES = P::STAGES;
+    constexpr bool TRANS = P::TRANS, GATED = P::GATED;
+    constexpr int kBK = 128;                             // bytes of k a step
+    constexpr int kWStage = TN * kBK, kXStage = TM * kBK;
+    constexpr int kWLoads = TN / 32, kXLoads = TM / 32;  // of 16 bytes a thread
+    constexpr int kStepLoads = kWLoads + kXLoads;
+    __shared__ __attribute__((aligned(256))) uint8_t lds[P::kLds];
+    uint8_t* const xlds = lds + STAGES * kWStage;
+
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wn = wave % P::WN, wm = wave / P::WN;
+    const int N = p.N, row_bytes = p.K * T::kBytes;
+    const int blocks = (row_bytes + kBK - 1) / kBK;
+    const GemmTiles tiles(p, TM, (N + P::kColumns - 1) / P::kColumns);
+
+    // What a tile's loads need.
+    struct Base {
+        const uint8_t* w;
+        const uint8_t* x;
+        int64_t wbytes, xbytes;      // 0: no tile
+        int col0, turn;
+    };
+    auto base_of = [&](const GemmTile& t) {
+        if (t.rows.expert < 0) return Base{p.w, p.a, 0, 0, 0, 0};
+        const int left = t.rows.end - t.rows.row0;
+        const int first = t.n * P::kColumns;
+        const int cols = N - first < P::kColumns ? N - first : P::kColumns;
+        Base b;
+        b.x = p.a + int64_t(t.rows.row0) * row_bytes;
+        b.xbytes = int64_t(left < TM ? left : TM) * row_bytes;
+        b.col0 = first;
+        b.turn = P::STREAM ? (t.rows.expert * 5 + t.n * 3) % blocks : 0;
+        if (TRANS) {
+            b.w = p.w + int64_t(t.rows.expert) * p.K * N * 2;
+            b.wbytes = 1;
+        } else {
+            b.w = p.w + (int64_t(t.rows.expert) * (GATED ? 2 * N : N) + first) * row_bytes;
+            b.wbytes = int64_t(cols) * row_bytes;
+        }
+        return b;
+    };
+
+    // LDS image of rows of 128 bytes: chunk c of 16 at slot c ^ (row / 2 % 8), so that
+    // the 16 lanes that read one chunk of 16 rows touch every bank once.  A load
+    // instruction fills 8 rows; its lanes fetch the chunks that belong there.
+    const int lchunk = (lane & 7) ^ (((wave & 1) * 4 + (lane >> 4)) & 7);
+    const uint32_t off0 = uint32_t(wave * 8 + lane / 8) * uint32_t(row_bytes) + lchunk * 16;
+    // Transposed weights: 64 rows of k of TN columns, in units of 64 bytes, unit u of
+    // row r at u ^ r % 4: a transposing read takes 8 rows x 64 bytes, rows 0..3 and
+    // 8..11 of 16, which then touch every bank twice, the least that 512 bytes can.
+    constexpr int kLanesPerRow = TN / 8, kRowsPerLoad = kWave / kLanesPerRow;
+    const int trow = wave * kRowsPerLoad + lane / kLanesPerRow;
+    const int tchunk = (lane & 3) | ((((lane % kLanesPerRow) >> 2) ^ (trow & 3)) << 2);
+
+    struct Source {
+        __amdgpu_buffer_rsrc_t r, up;      // up: gated
+        uint32_t off, group;
+    };
+    // Block of k of step s: the steps past the last one are all zeros.
+    auto block_of = [&](const Base& b, int s) {
+        const int k = s + b.turn;
+        return P::STREAM && k >= blocks ? k - blocks : k;
+    };
+    auto rows_source = [&](const uint8_t* base, const uint8_t* up, int64_t bytes, const Base& b, int s) {
+        const int k0 = block_of(b, s) * kBK;
+        const int left = s < blocks ? row_bytes - k0 : 0;
+        int off = off0;
+        hide(off);          // or every load's offset would take a register of its own
+        const int64_t use = left > 0 && bytes > k0 ? bytes - k0 : 0;
+        Source c;
+        c.r = buffer_rsrc(const_cast<uint8_t*>(base) + (use ? k0 : 0), use);
+        c.up = buffer_rsrc(const_cast<uint8_t*>(up) + (use ? k0 : 0), use);
+        c.off = uint32_t(off) | (lchunk * 16 >= left ? kOutside : 0);
+        c.group = uint32_t(row_bytes) * 32u;
+        return c;
+    };
+    auto weights_source = [&](const Base& b, int s) {
+        if (!TRANS) return rows_source(b.w, GATED ? b.w + int64_t(N) * row_bytes : b.w, b.wbytes, b, s);
+        const int k0 = block_of(b, s) * (kBK / 2);
+        const int left = s < blocks && b.wbytes ? p.K - k0 : 0;
+        int n = b.col0 + tchunk * 8;
+        hide(n);
+        const int64_t rows = left <= 0 ? 0 : left < kBK / 2 ? left : kBK / 2;
+        Source c;
+        c.r = c.up = buffer_rsrc(const_cast<uint8_t*>(b.w) + (rows ? int64_t(k0) * N * 2 : 0), rows * N * 2);
+        c.off = n < N ? (uint32_t(trow) * uint32_t(N) + uint32_t(n)) * 2u : kOutside;
+        c.group = uint32_t(N) * uint32_t(kRowsPerLoad * 8);
+        return c;
+    };
+    auto tokens_source = [&](const Base& b, int s) { return rows_source(b.x, b.x, b.xbytes, b, s); };
+    // load i of the weights: rows 32 i on, or gated groups of 32 rows that alternate
+    // between gate and up
+    auto issue_w = [&](const Source& c, uint8_t* to, int i) {
+        uint8_t* const at = to + i * 4096 + wave * 1024;
+        if (GATED) load16_to_lds<P::STREAM>(i & 1 ? c.up : c.r, at, c.off + uint32_t(i >> 1) * c.group);
+        else load16_to_lds<P::STREAM>(c.r, at, c.off + uint32_t(i) * c.group);
+    };
+    auto issue_x = [&](const Source& c, uint8_t* to, int i) {
+        load16_to_lds<false>(c.r, to + i * 4096 + wave * 1024, c.off + uint32_t(i) * c.group);
+    };
+
+    // Fragments of a quarter: 32 rows x 32 bytes of k, lane: row lt, the half lk.
+    const int lt = lane & 31, lk = lane >> 5, g = lane >> 4, l = lane & 15;
+    int foff[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) foff[q] = lt * kBK + (((2 * q + lk) ^ ((lt >> 1) & 7)) * 16);
+    const int woff = TRANS ? 0 : wn * FN * 32 * kBK, xoff = wm * FM * 32 * kBK;
+    // transposed: two transposing reads of rows 16 q + 8 lk .. + 3 and the four after them
+    int toff[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+        toff[i] = (lk * 8 + (l >> 2)) * (TN * 2) + ((wn * FN + i) ^ (l >> 2)) * 64 + (g & 1) * 32 +
+                  (l & 3) * 8;
+    struct Quarter {
+        u32x4 w[FN], x[FM];
+    };
+    constexpr int kWReads = TRANS ? 2 * FN : FN, kReads = kWReads + FM;
+    auto read = [&](uint8_t* ws, uint8_t* xs, int q, Quarter& f, int n) {
+        // the first weights, the tokens, the other weights: as they are used
+        constexpr int kFirst = TRANS ? 2 : 1;
+        if (n >= kFirst && n < kFirst + FM) {
+            f.x[n - kFirst] = load16(xs + xoff + (n - kFirst) * 32 * kBK + foff[q]);
+            return;
+        }
+        const int m = n < kFirst ? n : n - FM;
+        if (TRANS) {
+            const s16x4 v = read_transposed(ws + toff[m / 2] + (q * 16 + m % 2 * 4) * (TN * 2));
+            const u32x2 b = __builtin_bit_cast(u32x2, v);
+            f.w[m / 2][m % 2 * 2] = b[0];
+            f.w[m / 2][m % 2 * 2 + 1] = b[1];
+        } else {
+            f.w[m] = load16(ws + woff + m * 32 * kBK + foff[q]);
+        }
+    };
+    typename T::Acc acc[FN][FM];
+    // FN x FM matrix instructions on `f`, between them the reads of the next quarter
+    // (quarter q of stages ws and xs) and the loads [first, last) of `src` into `to`.
+    // Each matrix instruction is held in its place: the compiler would gather them
+    // otherwise, and run out of registers.  The stages are named restrict: it would
+    // wait for every load into LDS before a transposing read otherwise.
+    auto multiply = [&](const Quarter& f, uint8_t* __restrict__ ws, uint8_t* __restrict__ xs, int q,
+                        Quarter& next, const Source& src, uint8_t* __restrict__ to, bool weights,
+                        int first, int last) {
+        constexpr int kSlots = FN * FM;
+#pragma unroll
+        for (int n = 0; n < kSlots; ++n) {
+            const int i = n / FM, j = n % FM;
+            acc[i][j] = T::mfma(f.w[i], f.x[j], acc[i][j]);
+            pin(acc[i][j]);
+#pragma unroll
+            for (int r = n * kReads / kSlots; r < (n + 1) * kReads / kSlots; ++r) read(ws, xs, q, next, r);
+#pragma unroll
+            for (int r = first + n * (last - first) / kSlots;
+                 r < first + (n + 1) * (last - first) / kSlots; ++r) {
+                if (weights) issue_w(src, to, r);
+                else issue_x(src, to, r);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    GemmTile t = tiles.at(p, TM, 0);
+    if (t.rows.expert < 0) return;
+    // a tile's loads reach into the next one only
+    const int steps = blocks > STAGES - 1 ? blocks : STAGES - 1;
+    Base cur = base_of(t);
+#pragma unroll
+    for (int d = 0; d < STAGES - 1; ++d) {
+        const Source w = weights_source(cur, d), x = tokens_source(cur, d);
+#pragma unroll
+        for (int i = 0; i < kWLoads; ++i) issue_w(w, lds + d * kWStage, i);
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) issue_x(x, xlds + d * kXStage, i);
+    }
+    wait_and_barrier<(STAGES - 2) * kStepLoads>();
+    Quarter f0, f1;
+#pragma unroll
+    for (int n = 0; n < kReads; ++n) read(lds, xlds, 0, f0, n);
+    int wslot = 0, xslot = 0;                            // the stages of this step
+
+    for (int turn = 1;; ++turn) {
+        const GemmTile tnext = tiles.at(p, TM, turn);
+        const Base next = base_of(tnext);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) acc[i][j][c] = 0;
+        for (int s = 0; s < steps; ++s) {
+            const int wnext = wslot == STAGES - 1 ? 0 : wslot + 1;
+            const int wlast = wslot == 0 ? STAGES - 1 : wslot - 1;
+            const int xnext = xslot == STAGES - 2 ? 0 : xslot + 1;
+            const bool over = s + STAGES - 1 >= steps;
+            const int ahead = over ? s + STAGES - 1 - steps : s + STAGES - 1;
+            const Base& from = over ? next : cur;
+            uint8_t* const ws = lds + wslot * kWStage;
+            uint8_t* const xs = xlds + xslot * kXStage;
+            const Source w = weights_source(from, ahead);
+            uint8_t* const to = lds + wlast * kWStage;
+            multiply(f0, ws, xs, 1, f1, w, to, true, 0, kWLoads / 2);
+            multiply(f1, ws, xs, 2, f0, w, to, true, kWLoads / 2, kWLoads);
+            multiply(f0, ws, xs, 3, f1, w, to, true, 0, 0);
+            // newer than the next step's loads: those of STAGES - 3 steps, this step's
+            // weights, and in a tile's first step the last tile's stores
+            constexpr int kNewer = (STAGES - 3) * kStepLoads + kWLoads;
+            constexpr int kAfterStores = kNewer + P::kStores < 63 ? kNewer + P::kStores : 63;
+            if (s == 0 && turn > 1) wait_and_barrier<kAfterStores>();
+            else wait_and_barrier<kNewer>();
+            __builtin_amdgcn_sched_barrier(0);
+            const Source x = tokens_source(from, ahead);
+            multiply(f1, lds + wnext * kWStage, xlds + xnext * kXStage, 0, f0, x, xs, false, 0, kXLoads);
+            wslot = wnext;
+            xslot = xnext;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        // ---- epilogue: lane has tokens 32 j + lt of the wave's, weight rows 32 i + 8 q
+        // + 4 lk + 0..3 (register 4 q + 0..3).  32 tokens x NF fragments at a time go
+        // through LDS of the wave's own (the weights' stage that the last step left), so
+        // that stores write whole pieces of rows.  Every store is issued whatever the
+        // tile's edges (the descriptor drops what lies outside), so that their number is
+        // known above.
+        int el = lane;
+        hide(el);                // keeps the addresses below out of the main loop's registers
+        const int lane = el, lt = lane & 31, lk = lane >> 5;
+        const int rows = t.rows.end - t.rows.row0 < TM ? t.rows.end - t.rows.row0 : TM;
+        const int64_t row0 = t.rows.row0;
+        uint8_t* const scratch = lds + (wslot == 0 ? STAGES - 1 : wslot - 1) * kWStage;
+        constexpr int kPut = GATED ? FN / 2 : FN;
+        uint8_t* const mine = scratch + wave * (kPut * 2048);
+        const int col0 = t.n * P::kColumns + wn * kPut * 32;      // of the wave
+        auto put = [&](auto&& get, const __amdgpu_buffer_rsrc_t& r, int width, int at, int j) {
+            constexpr int kShift = kPut == 4 ? 0 : kPut == 2 ? 1 : 2, kMask = 4 * kPut - 1;
+#pragma unroll
+            for (int i = 0; i < kPut; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    float v[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] = get(i, 4 * q + c);
+                    const auto lo = __builtin_amdgcn_permlane32_swap(
+                        pack_bf16x2(v[0], v[1]), pack_bf16x2(v[4], v[5]), false, false);
+                    const auto hi = __builtin_amdgcn_permlane32_swap(
+                        pack_bf16x2(v[2], v[3]), pack_bf16x2(v[6], v[7]), false, false);
+                    *reinterpret_cast<u32x4*>(
+                        mine + lt * (64 * kPut) +
+                        (((i * 4 + q + lk) ^ ((lt >> kShift) & kMask)) * 16)) =
+                        u32x4{lo[0], hi[0], lo[1], hi[1]};
+                }
+            __builtin_amdgcn_wave_barrier();
+            constexpr int kRows = 16 / kPut;
+#pragma unroll
+            for (int k = 0; k < 2 * kPut; ++k) {
+                const int row = k * kRows + lane / (4 * kPut), c = lane % (4 * kPut);
+                const u32x4 v = load16(mine + row * (64 * kPut) + ((c ^ ((row >> kShift) & kMask)) * 16));
+                const int m = (wm * FM + j) * 32 + row, n = col0 + c * 8;
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    v, r, int(n < N ? (uint32_t(m) * uint32_t(width) + uint32_t(at + n)) * 2u : kOutside), 0,
+                    P::kStoreNt ? 2 : 0);
+            }
+            __builtin_amdgcn_wave_barrier();
+        };
+        // int8: the channels' scales and the tokens'
+        f32x4 wscale[T::kScaled ? FN : 1][4];
+        float token[FM];
+        if constexpr (T::kScaled) {
+            const int64_t expert = t.rows.expert;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = col0 + (GATED ? i >> 1 : i) * 32 + 8 * q + 4 * lk;
+                    const int64_t at = expert * (GATED ? 2 * N : N) + (GATED && (i & 1) ? N : 0);
+                    wscale[i][q] = f32x4{0, 0, 0, 0};
+                    if (n < N) wscale[i][q] = *reinterpret_cast<const f32x4*>(p.w_scale + at + n);
+                }
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                const int m = (wm * FM + j) * 32 + lt;
+                token[j] = m < rows ? p.a_scale[row0 + m] : 0.0f;
+            }
+        }
+        auto value = [&](int i, int j, int c) {
+            if constexpr (T::kScaled) return float(acc[i][j][c]) * wscale[i][c / 4][c % 4] * token[j];
+            else return float(acc[i][j][c]);
+        };
+        if constexpr (!GATED) {
+            const __amdgpu_buffer_rsrc_t r = buffer_rsrc(p.y + row0 * N, int64_t(rows) * N * 2);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) put([&](int i, int c) { return value(i, j, c); }, r, N, 0, j);
+        } else {
+            const __amdgpu_buffer_rsrc_t hr = buffer_rsrc(p.h + row0 * N, int64_t(rows) * N * 2);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                if constexpr (P::KIND == kGatedSaved) {
+                    const __amdgpu_buffer_rsrc_t yr =
+                        buffer_rsrc(p.y + row0 * 2 * N, int64_t(rows) * N * 4);
+                    put([&](int i, int c) { return value(2 * i, j, c); }, yr, 2 * N, 0, j);
+                    put([&](int i, int c) { return value(2 * i + 1, j, c); }, yr, 2 * N, N, j);
+                }
+                put([&](int i, int c) {
+                    const float gate = value(2 * i, j, c);
+                    return gate * sigmoid(gate) * value(2 * i + 1, j, c);
+                }, hr, N, 0, j);
+            }
+        }
+        if (tnext.rows.expert < 0) break;
+        wait_and_barrier<63>();     // the scratch has been read before the next loads into it
+        t = tnext;
+        cur = next;
+    }
+    wait_and_barrier<0>();          // no load into LDS outlives the workgroup
+}
+
+template <class P>
+hipError_t launch_product(ProductArgs p, hipStream_t s)
+{
+    uint32_t grid = gemm_tiles(p, P::TM, P::kColumns);
+    if (!grid) return hipErrorInvalidConfiguration;
+    const uint32_t most = device_cu_count() / 8 * 8 * P::kOccupancy;
+    grid = grid < most || most == 0 ? grid : most;
+    EP_LAUNCH((expert_product_kernel<P>), dim3(grid), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace ep

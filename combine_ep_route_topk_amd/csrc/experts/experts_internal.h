@@ -62,6 +62,7 @@ hipError_t launch_expert_swiglu_int8(const int8_t* a, const float* a_scale, cons
 // ----------------------------------------------------------------- device
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -133,7 +134,8 @@ __device__ __forceinline__ void wait_and_barrier() {
 }
 
 // Keeps a matrix instruction's result, and so the instruction, in its place.
-__device__ __forceinline__ void pin(f32x16& v) {
+template <class V>
+__device__ __forceinline__ void pin(V& v) {
 #if defined(__HIP_DEVICE_COMPILE__)
     asm volatile("" : "+a"(v));
 #endif
