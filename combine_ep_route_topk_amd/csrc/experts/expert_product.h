@@ -43,6 +43,7 @@ struct ProductArgs {
 
 struct Bf16 {
     typedef f32x16 Acc;
+    typedef f32x4 Quad;
     static constexpr int kBytes = 2;
     static constexpr bool kScaled = false;
     static __device__ __forceinline__ Acc mfma(u32x4 w, u32x4 x, Acc c) {
@@ -52,6 +53,7 @@ struct Bf16 {
 };
 struct Int8 {
     typedef i32x16 Acc;
+    typedef i32x4 Quad;
     static constexpr int kBytes = 1;
     static constexpr bool kScaled = true;
     static __device__ __forceinline__ Acc mfma(u32x4 w, u32x4 x, Acc c) {
@@ -408,6 +410,235 @@ hipError_t launch_product(ProductArgs p, hipStream_t s)
     const uint32_t most = device_cu_count() / 8 * 8 * P::kOccupancy;
     grid = grid < most || most == 0 ? grid : most;
     EP_LAUNCH((expert_product_kernel<P>), dim3(grid), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------- few tiles
+// Few rows against few weight rows: tiles of 32 FN weight rows (gated, FN = 1: 16 of
+// the gate and their 16 up rows) x 32 FM tokens, and the four waves of a workgroup
+// share k instead: wave v takes the blocks v, v + 4, .. of 128 bytes, through stages
+// of its own, without a barrier.  Their sums meet in LDS, in the waves' order; wave v
+// finishes the rows 8 v .. 8 v + 7 of each 32.
+template <class T_, ProductKind KIND_, int FN_, int FM_, int STAGES_>
+struct NarrowShape {
+    typedef T_ T;
+    static constexpr ProductKind KIND = KIND_;
+    static constexpr int FN = FN_, FM = FM_, STAGES = STAGES_;
+    static constexpr bool TRANS = KIND == kTransposed, GATED = KIND >= kGated;
+    static constexpr int TN = 32 * FN, TM = 32 * FM;
+    static constexpr int kColumns = GATED ? TN / 2 : TN;
+    static constexpr int kLds = 4 * STAGES * (TN + TM) * 128;
+    static constexpr int kOccupancy = kLds > 80 * 1024 ? 1 : kLds > 160 * 1024 / 3 ? 2 : 3;
+    static constexpr bool kHalves = GATED && FN == 1;     // gate and up share a fragment
+    static_assert(!GATED || FN <= 2, "gate rows, then their up rows");
+    static_assert(FN <= 2, "a row of a transposed stage is a line at most");
+    static_assert(4 * FN * FM * 4096 <= kLds, "the waves' sums");
+};
+
+template <class P>
+__global__ __launch_bounds__(256, P::kOccupancy) void expert_narrow_kernel(ProductArgs p)
+{
+    typedef typename P::T T;
+    constexpr int FN = P::FN, FM = P::FM, STAGES = P::STAGES;
+    constexpr bool TRANS = P::TRANS, GATED = P::GATED;
+    constexpr int kBK = 128, kStage = (P::TN + P::TM) * kBK, kLoads = 4 * (FN + FM);
+    __shared__ __attribute__((aligned(256))) uint8_t lds[P::kLds];
+
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int N = p.N, row_bytes = p.K * T::kBytes;
+    const int blocks = (row_bytes + kBK - 1) / kBK;
+    const GemmTile tile = GemmTiles(p, P::TM, (N + P::kColumns - 1) / P::kColumns).at(p, P::TM, 0);
+    const RowTile t = tile.rows;
+    if (t.expert < 0) return;
+    const int rows = t.end - t.row0 < P::TM ? t.end - t.row0 : P::TM;
+    const int col0 = tile.n * P::kColumns;
+    const int cols = N - col0 < P::kColumns ? N - col0 : P::kColumns;
+    // every tile starts at another block of k: rows a power of two apart would keep
+    // to a few memory channels
+    // (tiles of half a line stay together)
+    const int turn = (t.expert * 5 + (TRANS && FN == 1 ? tile.n / 2 : tile.n) * 3) % blocks;
+    uint8_t* const mine = lds + wave * STAGES * kStage;
+
+    const __amdgpu_buffer_rsrc_t xr =
+        buffer_rsrc(const_cast<uint8_t*>(p.a) + int64_t(t.row0) * row_bytes, int64_t(rows) * row_bytes);
+    const uint8_t* const w0 =
+        TRANS ? p.w + int64_t(t.expert) * p.K * N * 2
+              : p.w + (int64_t(t.expert) * (GATED ? 2 * N : N) + col0) * row_bytes;
+    const __amdgpu_buffer_rsrc_t wr =
+        buffer_rsrc(const_cast<uint8_t*>(w0), TRANS ? 0 : int64_t(cols) * row_bytes);
+    const __amdgpu_buffer_rsrc_t ur = buffer_rsrc(
+        const_cast<uint8_t*>(w0) + (GATED ? int64_t(N) * row_bytes : 0), int64_t(cols) * row_bytes);
+
+    // Rows of 128 bytes: load i fills rows 8 i .. 8 i + 7, chunk c of row r at c ^ r /
+    // 2 % 8; transposed weights are 64 rows of k of a line (FN = 2), unit u (64 bytes) of
+    // row r at u ^ r / 2 % 2, or half of one.
+    const int lrow = lane / 8;
+    auto load = [&](int step, uint8_t* to) {
+        const bool some = step < blocks;
+        int b = step + turn;
+        b = b < blocks ? b : b - blocks;
+        const int k0 = some ? b * kBK : row_bytes;
+#pragma unroll
+        for (int i = 0; i < 4 * FN; ++i) {
+            if (TRANS) {
+                const int row = FN == 2 ? i * 8 + lrow : i * 16 + lane / 4;
+                const int chunk =
+                    (lane & 3) | (FN == 2 ? (((lane & 7) >> 2) ^ (row >> 1 & 1)) << 2 : 0);
+                const int left = p.K - k0 / 2, n = col0 + chunk * 8;
+                const __amdgpu_buffer_rsrc_t r = buffer_rsrc(
+                    const_cast<uint8_t*>(w0) + int64_t(some ? k0 / 2 : 0) * N * 2,
+                    int64_t(!some ? 0 : left < 64 ? left : 64) * N * 2);
+                load16_to_lds<true>(r, to + i * 1024,
+                                    n < N ? (uint32_t(row) * uint32_t(N) + uint32_t(n)) * 2u : kOutside);
+            } else {
+                // gated: the gate rows, then their up rows
+                const int kc = k0 + ((lane & 7) ^ ((i & 1) * 4 + (lane >> 4))) * 16;
+                const int row = (GATED ? i % (2 * FN) : i) * 8 + lrow;
+                load16_to_lds<true>(GATED && i >= 2 * FN ? ur : wr, to + i * 1024,
+                                    kc < row_bytes ? uint32_t(row) * uint32_t(row_bytes) + uint32_t(kc)
+                                                   : kOutside);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * FM; ++i) {
+            const int kc = k0 + ((lane & 7) ^ ((i & 1) * 4 + (lane >> 4))) * 16;
+            load16_to_lds<false>(xr, to + P::TN * kBK + i * 1024,
+                                 kc < row_bytes ? uint32_t(i * 8 + lrow) * uint32_t(row_bytes) + uint32_t(kc)
+                                                : kOutside);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int lt = lane & 31, lk = lane >> 5, g = lane >> 4, l = lane & 15;
+    auto rows_fragment = [&](const uint8_t* from, int q) {
+        return load16(from + lt * kBK + (((2 * q + lk) ^ ((lt >> 1) & 7)) * 16));
+    };
+    auto weights_fragment = [&](uint8_t* __restrict__ from, int i, int q) {
+        if (!TRANS) return rows_fragment(from + i * 32 * kBK, q);
+        u32x4 v;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int row = q * 16 + lk * 8 + c * 4 + (l >> 2);
+            const u32x2 b = __builtin_bit_cast(
+                u32x2, read_transposed(from + row * (64 * FN) + (FN == 2 ? (i ^ (row >> 1 & 1)) * 64 : 0) +
+                                       (g & 1) * 32 + (l & 3) * 8));
+            v[2 * c] = b[0];
+            v[2 * c + 1] = b[1];
+        }
+        return v;
+    };
+
+    typename T::Acc acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) acc[i][j][c] = 0;
+    auto multiply = [&](uint8_t* __restrict__ from) {
+        u32x4 w[FN][4], x[FM][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) w[i][q] = weights_fragment(from, i, q);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) x[j][q] = rows_fragment(from + (P::TN + j * 32) * kBK, q);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] = T::mfma(w[i][q], x[j][q], acc[i][j]);
+    };
+#pragma unroll
+    for (int d = 0; d < STAGES - 1; ++d) load(wave + 4 * d, mine + d * kStage);
+    const int count = (blocks - wave + 3) / 4;       // of this wave; may be 0
+    for (int s0 = 0; s0 < count; s0 += STAGES) {
+#pragma unroll
+        for (int d = 0; d < STAGES; ++d) {            // past the last block: zeros
+            // step s0 + d has landed, the step before has been read
+            wait_loads<(STAGES - 2) * kLoads>();
+            load(wave + 4 * (s0 + d + STAGES - 1), mine + (d + STAGES - 1) % STAGES * kStage);
+            multiply(mine + d * kStage);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    wait_and_barrier<0>();          // no load is on its way, every stage has been read
+
+    // the waves' sums: 4 values of a lane for each fragment and q, [wave][fragment][q][lane]
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<typename T::Quad*>(lds + (((wave * FN + i) * FM + j) * 4 + q) * 1024 +
+                                                     lane * 16) =
+                    typename T::Quad{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                     acc[i][j][4 * q + 3]};
+    __syncthreads();
+    // lane: token 32 j + lt, weight rows 32 i + 8 wave + 4 lk + 0..3
+    const int n = col0 + wave * 8 + lk * 4;           // of fragment 0
+    auto store = [&](uint16_t* to, f32x4 v) {
+        *reinterpret_cast<u32x2*>(to) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    };
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int m = j * 32 + lt;
+        if (m >= rows) continue;
+        const int64_t row = t.row0 + m;
+        const float token = T::kScaled ? p.a_scale[row] : 1.0f;
+        // rows q of fragment i; channel: of y, or of [g; u]
+        auto value = [&](int i, int q, int channel) {
+            typename T::Quad sum;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const auto part = *reinterpret_cast<const typename T::Quad*>(
+                    lds + (((k * FN + i) * FM + j) * 4 + q) * 1024 + lane * 16);
+                if (k == 0) sum = part;
+                else
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum[c] += part[c];
+            }
+            f32x4 v;
+            if constexpr (T::kScaled) {
+                const f32x4 scale = *reinterpret_cast<const f32x4*>(
+                    p.w_scale + int64_t(t.expert) * (GATED ? 2 * N : N) + channel);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = float(sum[c]) * scale[c] * token;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = sum[c];
+            }
+            return v;
+        };
+        if constexpr (!GATED) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+                if (n + i * 32 < N) store(p.y + row * N + n + i * 32, value(i, wave, n + i * 32));
+        } else {
+            if (n >= N || (P::kHalves && wave >= 2)) continue;
+            const f32x4 gate = value(0, wave, n);
+            const f32x4 up = P::kHalves ? value(0, wave + 2, N + n) : value(FN - 1, wave, N + n);
+            if constexpr (P::KIND == kGatedSaved) {
+                store(p.y + row * 2 * N + n, gate);
+                store(p.y + row * 2 * N + N + n, up);
+            }
+            f32x4 h;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) h[c] = gate[c] * sigmoid(gate[c]) * up[c];
+            store(p.h + row * N + n, h);
+        }
+    }
+}
+
+template <class P>
+hipError_t launch_narrow(ProductArgs p, hipStream_t s)
+{
+    const uint32_t grid = gemm_tiles(p, P::TM, P::kColumns);
+    if (!grid || uint64_t(grid) * 256 >= (uint64_t(1) << 31)) return hipErrorInvalidConfiguration;
+    EP_LAUNCH((expert_narrow_kernel<P>), dim3(grid), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

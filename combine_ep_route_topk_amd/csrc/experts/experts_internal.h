@@ -133,6 +133,15 @@ __device__ __forceinline__ void wait_and_barrier() {
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
+// The wait alone, for loads into LDS of the wave's own.
+template <int VM>
+__device__ __forceinline__ void wait_loads() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | (15 << 8) | ((VM >> 4) << 14));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Keeps a matrix instruction's result, and so the instruction, in its place.
 template <class V>
 __device__ __forceinline__ void pin(V& v) {
