@@ -3,6 +3,7 @@
 // which kernel its sizes reach.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 namespace ep {
@@ -70,6 +71,106 @@ inline GemmKernel choose_gemm(int64_t S, int64_t N, int64_t E, bool gated, int64
     // a last, partly filled tile for every other expert
     const int64_t few = (S / 32 + used / 2) * ((N + 255) / 256);
     return few <= cus ? kGemm32x256 : kGemm64x256;
+}
+
+// ------------------------------------------------------------- bf16 and int8 products
+// Tiles of so many weight rows x tokens: persistent ones of the kernel whose waves
+// split the tile, and narrow ones of the kernel whose waves share k.
+enum ProductKernel {
+    kProduct256x256,
+    kProduct256x128,
+    kProduct128x128,
+    kProduct256x64,
+    kProduct128x64,
+    kNarrow64x64,
+    kNarrow32x64,
+    kNarrow32x32,
+    kProductKernels,
+};
+
+// What a tile takes on MI355X, us: `tile` and `step` for each 128 bytes of k, of the
+// tiles that the CUs work on at once.  Fitted to 3459 measured sizes (1 to 64 experts of 1
+// to 2500 rows on average, even and as even picks fall, 64 to 8192 weight rows, 128 to
+// 8192 values of k, bf16 either way round, gated and int8, weights from memory): the
+// kernel chosen by them takes 2% longer than the best one on average, 20% at the 97th
+// percentile, 60% at the worst.  Without the 256 x 256 tiles the best one of the others takes
+// 4% longer on average, without 256 x 128 1%, 128 x 128 3%, 128 x 64 1%, the narrow ones
+// 1 to 5%.  For instance, us (bf16, weights from memory):
+//                                        256x256 256x128 128x128 256x64 128x64 32x32
+//   8 experts x 4096 x 7168, 8 rows each                  121     93     70     77
+//   16 x 2816 x 4096, 64                                  100     61     77    131
+//   8 x 4096 x 7168, 160                   136     112    132
+//   8 x 4096 x 7168, 500                   179     215    251
+//   1 x 4096 x 4096, 1024                          56      49     53
+//   4 x 2048 x 4096, 8                                            44     28     14
+//   1 x 4096 x 7168, 8                                            78     46     16
+struct ProductTile {
+    int weights, tokens;
+    int per_cu;              // workgroups a CU; 0: not persistent, about one at a time
+    double step, tile;
+};
+inline const ProductTile& product_tile(int kernel)
+{
+    static const ProductTile tiles[kProductKernels] = {
+        {256, 256, 1, 1.35, 6.7}, {256, 128, 1, 1.17, 2.1}, {128, 128, 2, 1.26, 0.9},
+        {256, 64, 1, 0.82, 1.4},  {128, 64, 1, 0.41, 1.7},  {64, 64, 0, 0.375, 2.0},
+        {32, 64, 0, 0.355, 1.85}, {32, 32, 0, 0.325, 1.85},
+    };
+    return tiles[kernel];
+}
+constexpr double kStepAlone128x128 = 0.82;      // one workgroup on each CU
+constexpr double kBytesPerUs = 6.6e6;
+
+// N: columns of the result; row_bytes: of a row of k; gated: 2 N weight rows.  At
+// most S experts have rows; picks that fall evenly give them their square root more
+// or less, and the fuller ones count.  Where memory bounds several alike, the largest
+// tile.
+inline ProductKernel choose_product(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bool gated,
+                                    int64_t cus)
+{
+    const double used = double(S < E ? S : E), rows = double(S) / used;
+    const double blocks = double((row_bytes + 127) / 128);
+    const double bytes = double(row_bytes) * (used * double(gated ? 2 * N : N) + double(S)) +
+                         2.0 * double(S) * double(N);
+    const double slots = double(cus > 8 ? cus / 8 : 1);      // CUs of an XCD
+    ProductKernel best = kProduct256x256;
+    double least = 0.0;
+    for (int k = 0; k < kProductKernels; ++k) {
+        const ProductTile& t = product_tile(k);
+        const int64_t columns = gated ? t.weights / 2 : t.weights;
+        double row_tiles = used * ceil((rows + sqrt(rows)) / t.tokens);
+        if (row_tiles > double(S)) row_tiles = double(S);
+        const double tiles = ceil(row_tiles * double((N + columns - 1) / columns));
+        double rounds, step = t.step;
+        if (t.per_cu == 0) {
+            rounds = tiles / (8.0 * slots);
+            if (rounds < 1.0) rounds = 1.0;
+        } else {
+            const double one = ceil(ceil(tiles / 8.0) / slots);
+            rounds = ceil(one / t.per_cu);
+            if (t.per_cu > 1 && one <= 1.0) step = kStepAlone128x128;
+        }
+        double us = rounds * (t.tile + blocks * step);
+        if (us < bytes / kBytesPerUs) us = bytes / kBytesPerUs;
+        if (k == 0 || us < least) {
+            least = us;
+            best = ProductKernel(k);
+        }
+    }
+    return best;
+}
+
+// Whether the tiles of 64 tokens read the weights past the caches: each of them once
+// (as many rows as one tile holds), more than the caches keep until the next call, in
+// whole lines.  Past / through the caches: more than 64 MB, up to 48 rows an expert 0.89
+// to 0.93, 48 to 64 0.92 to 0.97, more rows 1.01 to 1.06; less than 32 MB 1.08; rows of k that
+// do not begin on lines 1.02 to 1.11.
+inline bool product_past_caches(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bool gated,
+                                int64_t line_bytes)
+{
+    const int64_t used = S < E ? S : E;
+    return S <= 64 * used && (gated ? 2 : 1) * E * N * row_bytes > (int64_t(64) << 20) &&
+           line_bytes % 128 == 0;
 }
 
 // ------------------------------------------------------------- weight gradients

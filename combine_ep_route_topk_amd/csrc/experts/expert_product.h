@@ -64,12 +64,13 @@ struct Int8 {
 
 enum ProductKind { kPlain, kTransposed, kGated, kGatedSaved };
 
-template <class T_, ProductKind KIND_, int FN_, int FM_, int WN_, int STAGES_, bool STREAM_>
+template <class T_, ProductKind KIND_, int FN_, int FM_, int WN_, int STAGES_, bool TURN_, bool NT_>
 struct ProductShape {
     typedef T_ T;
     static constexpr ProductKind KIND = KIND_;
     static constexpr int FN = FN_, FM = FM_, WN = WN_, STAGES = STAGES_;
-    static constexpr bool STREAM = STREAM_;      // the weights past the caches, k from a turn of its own
+    static constexpr bool TURN = TURN_;          // every tile of weights starts at another k
+    static constexpr bool NT = NT_;              // the weights past the caches
     static constexpr bool TRANS = KIND == kTransposed, GATED = KIND >= kGated;
     static constexpr int TN = 32 * FN * WN, TM = 32 * FM * (4 / WN);
     static constexpr int kColumns = GATED ? TN / 2 : TN;      // of y or h
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
         b.x = p.a + int64_t(t.rows.row0) * row_bytes;
         b.xbytes = int64_t(left < TM ? left : TM) * row_bytes;
         b.col0 = first;
-        b.turn = P::STREAM ? (t.rows.expert * 5 + t.n * 3) % blocks : 0;
+        b.turn = P::TURN ? (t.rows.expert * 5 + t.n * 3) % blocks : 0;
         if (TRANS) {
             b.w = p.w + int64_t(t.rows.expert) * p.K * N * 2;
             b.wbytes = 1;
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     // Block of k of step s: the steps past the last one are all zeros.
     auto block_of = [&](const Base& b, int s) {
         const int k = s + b.turn;
-        return P::STREAM && k >= blocks ? k - blocks : k;
+        return P::TURN && k >= blocks ? k - blocks : k;
     };
     auto rows_source = [&](const uint8_t* base, const uint8_t* up, int64_t bytes, const Base& b, int s) {
         const int k0 = block_of(b, s) * kBK;
@@ -181,8 +182,8 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     // between gate and up
     auto issue_w = [&](const Source& c, uint8_t* to, int i) {
         uint8_t* const at = to + i * 4096 + wave * 1024;
-        if (GATED) load16_to_lds<P::STREAM>(i & 1 ? c.up : c.r, at, c.off + uint32_t(i >> 1) * c.group);
-        else load16_to_lds<P::STREAM>(c.r, at, c.off + uint32_t(i) * c.group);
+        if (GATED) load16_to_lds<P::NT>(i & 1 ? c.up : c.r, at, c.off + uint32_t(i >> 1) * c.group);
+        else load16_to_lds<P::NT>(c.r, at, c.off + uint32_t(i) * c.group);
     };
     auto issue_x = [&](const Source& c, uint8_t* to, int i) {
         load16_to_lds<false>(c.r, to + i * 4096 + wave * 1024, c.off + uint32_t(i) * c.group);
@@ -489,13 +490,13 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_narrow_kernel(Produ
                 const __amdgpu_buffer_rsrc_t r = buffer_rsrc(
                     const_cast<uint8_t*>(w0) + int64_t(some ? k0 / 2 : 0) * N * 2,
                     int64_t(!some ? 0 : left < 64 ? left : 64) * N * 2);
-                load16_to_lds<true>(r, to + i * 1024,
+                load16_to_lds<false>(r, to + i * 1024,
                                     n < N ? (uint32_t(row) * uint32_t(N) + uint32_t(n)) * 2u : kOutside);
             } else {
                 // gated: the gate rows, then their up rows
                 const int kc = k0 + ((lane & 7) ^ ((i & 1) * 4 + (lane >> 4))) * 16;
                 const int row = (GATED ? i % (2 * FN) : i) * 8 + lrow;
-                load16_to_lds<true>(GATED && i >= 2 * FN ? ur : wr, to + i * 1024,
+                load16_to_lds<false>(GATED && i >= 2 * FN ? ur : wr, to + i * 1024,
                                     kc < row_bytes ? uint32_t(row) * uint32_t(row_bytes) + uint32_t(kc)
                                                    : kOutside);
             }

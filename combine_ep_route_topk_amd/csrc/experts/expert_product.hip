@@ -6,11 +6,31 @@
 namespace ep {
 namespace {
 
+template <class T, ProductKind KIND, int FN, int FM, int WN, int STAGES>
+hipError_t launch_rows(const ProductArgs& p, bool past_caches, hipStream_t s)
+{
+    if (past_caches) return launch_product<ProductShape<T, KIND, FN, FM, WN, STAGES, true, true>>(p, s);
+    return launch_product<ProductShape<T, KIND, FN, FM, WN, STAGES, true, false>>(p, s);
+}
+
 template <class T, ProductKind KIND>
 hipError_t launch(const ProductArgs& p, hipStream_t s)
 {
-    if (int64_t(p.S) >= 160 * int64_t(p.E)) return launch_product<ProductShape<T, KIND, 4, 4, 2, 3, false>>(p, s);
-    return launch_product<ProductShape<T, KIND, 2, 1, 4, 4, true>>(p, s);
+    constexpr bool kIsGated = KIND >= kGated;
+    const int64_t row_bytes = int64_t(p.K) * T::kBytes;
+    const int64_t line_bytes = KIND == kTransposed ? int64_t(p.N) * T::kBytes : row_bytes;
+    const bool past = product_past_caches(p.S, p.N, row_bytes, p.E, kIsGated, line_bytes);
+    switch (choose_product(p.S, p.N, row_bytes, p.E, kIsGated, device_cu_count())) {
+        case kProduct256x256: return launch_product<ProductShape<T, KIND, 4, 4, 2, 3, false, false>>(p, s);
+        case kProduct256x128: return launch_product<ProductShape<T, KIND, 4, 2, 2, 3, false, false>>(p, s);
+        case kProduct128x128: return launch_product<ProductShape<T, KIND, 2, 2, 2, 3, false, false>>(p, s);
+        case kProduct256x64: return launch_rows<T, KIND, 2, 2, 4, 3>(p, past, s);
+        case kProduct128x64: return launch_rows<T, KIND, 2, 1, 2, 4>(p, past, s);
+        case kNarrow64x64: return launch_narrow<NarrowShape<T, KIND, 2, 2, 2>>(p, s);
+        case kNarrow32x64: return launch_narrow<NarrowShape<T, KIND, 1, 2, 3>>(p, s);
+        case kNarrow32x32: return launch_narrow<NarrowShape<T, KIND, 1, 1, 3>>(p, s);
+        default: return hipErrorInvalidConfiguration;
+    }
 }
 
 }  // namespace
