@@ -88,22 +88,24 @@ enum ProductKernel {
     kProductKernels,
 };
 
-// What a tile takes on MI355X, us: `tile` and `step` for each 128 bytes of k, of the
-// tiles that the CUs work on at once.  Fitted to 3459 measured sizes (1 to 64 experts of 1
-// to 2500 rows on average, even and as even picks fall, 64 to 8192 weight rows, 128 to
-// 8192 values of k, bf16 either way round, gated and int8, weights from memory): the
-// kernel chosen by them takes 2% longer than the best one on average, 20% at the 97th
-// percentile, 60% at the worst.  Without the 256 x 256 tiles the best one of the others takes
-// 4% longer on average, without 256 x 128 1%, 128 x 128 3%, 128 x 64 1%, the narrow ones
-// 1 to 5%.  For instance, us (bf16, weights from memory):
-//                                        256x256 256x128 128x128 256x64 128x64 32x32
-//   8 experts x 4096 x 7168, 8 rows each                  121     93     70     77
-//   16 x 2816 x 4096, 64                                  100     61     77    131
-//   8 x 4096 x 7168, 160                   136     112    132
-//   8 x 4096 x 7168, 500                   179     215    251
-//   1 x 4096 x 4096, 1024                          56      49     53
-//   4 x 2048 x 4096, 8                                            44     28     14
-//   1 x 4096 x 7168, 8                                            78     46     16
+// What a tile takes on MI355X, us: `tile`, and `step` for each 128 bytes of k, of the
+// tiles that the CUs work on at once.  Fitted to 4455 measured sizes (1 to 64 experts of
+// 1 to 2500 rows on average, even, as even picks fall or by a Zipf law, 64 to 8192 weight
+// rows, 128 to 8192 values of k, bf16 either way round, gated and int8, weights from
+// memory): the kernel chosen by them takes 2% longer than the best one on average (3% by the
+// Zipf law), 20% at the 97th percentile, 2.4 times at the worst (a Zipf law, which sizes
+// do not tell).  Without the 256 x 256 tiles the best of the others takes 2% longer on average
+// and 50% at most, without 256 x 128 1% and 38%, 128 x 128 1% and 46%, 256 x 64 0.5% and
+// 17%, 128 x 64 1.5% and 38%, without the narrow ones 1.6, 1 and 7%, and up to 72%.  For
+// instance, us (bf16, weights from memory):
+//                                          256x256 256x128 128x128 256x64 128x64 32x32
+//   8 experts x 4096 x 7168, 8 rows each                             93     70     77
+//   16 x 2816 x 4096, 64                                     79      61     77    131
+//   16 x 2816 x 4096, 128                    89      67      99
+//   8 x 4096 x 7168, 500                    186     221     257
+//   1 x 4096 x 4096, 1024                    78      54      43      48
+//   4 x 2048 x 4096, 8                                               44     28     14
+//   1 x 4096 x 7168, 8                                               78     46     16
 struct ProductTile {
     int weights, tokens;
     int per_cu;              // workgroups a CU; 0: not persistent, about one at a time
@@ -112,13 +114,13 @@ struct ProductTile {
 inline const ProductTile& product_tile(int kernel)
 {
     static const ProductTile tiles[kProductKernels] = {
-        {256, 256, 1, 1.35, 6.7}, {256, 128, 1, 1.17, 2.1}, {128, 128, 2, 1.26, 0.9},
-        {256, 64, 1, 0.82, 1.4},  {128, 64, 1, 0.41, 1.7},  {64, 64, 0, 0.375, 2.0},
-        {32, 64, 0, 0.355, 1.85}, {32, 32, 0, 0.325, 1.85},
+        {256, 256, 1, 1.355, 7.7}, {256, 128, 1, 0.94, 3.7}, {128, 128, 2, 1.455, 1.27},
+        {256, 64, 1, 0.80, 2.1},   {128, 64, 1, 0.41, 1.57}, {64, 64, 0, 0.385, 1.6},
+        {32, 64, 0, 0.34, 1.73},   {32, 32, 0, 0.34, 1.68},
     };
     return tiles[kernel];
 }
-constexpr double kStepAlone128x128 = 0.82;      // one workgroup on each CU
+constexpr double kStepAlone128x128 = 0.80;      // one workgroup on each CU
 constexpr double kBytesPerUs = 6.6e6;
 
 // N: columns of the result; row_bytes: of a row of k; gated: 2 N weight rows.  At
@@ -160,16 +162,17 @@ inline ProductKernel choose_product(int64_t S, int64_t N, int64_t row_bytes, int
     return best;
 }
 
-// Whether the tiles of 64 tokens read the weights past the caches: each of them once
-// (as many rows as one tile holds), more than the caches keep until the next call, in
-// whole lines.  Past / through the caches: more than 64 MB, up to 48 rows an expert 0.89
-// to 0.93, 48 to 64 0.92 to 0.97, more rows 1.01 to 1.06; less than 32 MB 1.08; rows of k that
-// do not begin on lines 1.02 to 1.11.
+// Whether tiles of so many tokens read the weights past the caches: each of them once
+// (no more rows than one tile holds), more than the caches keep until the next call, in
+// whole lines.  Past / through the caches, weights from memory: 0.89 to 0.96 with 64 MB and
+// more, 0.87 to 0.98 with less (but 33 MB that the last call left there would take 15 us
+// instead of 11); with more rows than a tile holds 1.0 to 1.2; with rows of k that do not
+// begin on lines 1.0 to 1.15.
 inline bool product_past_caches(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bool gated,
-                                int64_t line_bytes)
+                                int64_t line_bytes, int64_t tokens)
 {
     const int64_t used = S < E ? S : E;
-    return S <= 64 * used && (gated ? 2 : 1) * E * N * row_bytes > (int64_t(64) << 20) &&
+    return S <= tokens * used && (gated ? 2 : 1) * E * N * row_bytes > (int64_t(64) << 20) &&
            line_bytes % 128 == 0;
 }
 
