@@ -103,33 +103,6 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     const int blocks = (row_bytes + kBK - 1) / kBK;
     const GemmTiles tiles(p, TM, (N + P::kColumns - 1) / P::kColumns);
 
-    // What a tile's loads need.
-    struct Base {
-        const uint8_t* w;
-        const uint8_t* x;
-        int64_t wbytes, xbytes;      // 0: no tile
-        int col0, turn;
-    };
-    auto base_of = [&](const GemmTile& t) {
-        if (t.rows.expert < 0) return Base{p.w, p.a, 0, 0, 0, 0};
-        const int left = t.rows.end - t.rows.row0;
-        const int first = t.n * P::kColumns;
-        const int cols = N - first < P::kColumns ? N - first : P::kColumns;
-        Base b;
-        b.x = p.a + int64_t(t.rows.row0) * row_bytes;
-        b.xbytes = int64_t(left < TM ? left : TM) * row_bytes;
-        b.col0 = first;
-        b.turn = P::TURN ? (t.rows.expert * 5 + t.n * 3) % blocks : 0;
-        if (TRANS) {
-            b.w = p.w + int64_t(t.rows.expert) * p.K * N * 2;
-            b.wbytes = 1;
-        } else {
-            b.w = p.w + (int64_t(t.rows.expert) * (GATED ? 2 * N : N) + first) * row_bytes;
-            b.wbytes = int64_t(cols) * row_bytes;
-        }
-        return b;
-    };
-
     // LDS image of rows of 128 bytes: chunk c of 16 at slot c ^ (row / 2 % 8), so that
     // the 16 lanes that read one chunk of 16 rows touch every bank once.  A load
     // instruction fills 8 rows; its lanes fetch the chunks that belong there.
@@ -142,42 +115,63 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     const int trow = wave * kRowsPerLoad + lane / kLanesPerRow;
     const int tchunk = (lane & 3) | ((((lane % kLanesPerRow) >> 2) ^ (trow & 3)) << 2);
 
+    // Where the stream of loads is: a tile, its next block of k, and how many blocks are
+    // left (none: zeros).
+    struct Cursor {
+        const uint8_t* w;
+        const uint8_t* x;
+        int wbytes, xbytes;      // 0: no tile; transposed weights: of a row of k
+        int k, left;
+        uint32_t woff;           // transposed
+    };
+    auto start = [&](const GemmTile& t) {
+        const bool some = t.rows.expert >= 0;
+        const int rows = t.rows.end - t.rows.row0, first = t.n * P::kColumns;
+        const int cols = N - first < P::kColumns ? N - first : P::kColumns;
+        Cursor c;
+        c.x = p.a + (some ? int64_t(t.rows.row0) * row_bytes : 0);
+        c.xbytes = some ? (rows < TM ? rows : TM) * row_bytes : 0;
+        const int64_t row = int64_t(some ? t.rows.expert : 0) * (TRANS ? p.K : GATED ? 2 * N : N);
+        c.w = p.w + (TRANS ? row * N * 2 : (row + (some ? first : 0)) * row_bytes);
+        c.wbytes = !some ? 0 : TRANS ? N * 2 : cols * row_bytes;
+        c.k = P::TURN && some ? (t.rows.expert * 5 + t.n * 3) % blocks : 0;
+        c.left = blocks;
+        const int n = first + tchunk * 8;
+        c.woff = n < N ? (uint32_t(trow) * uint32_t(N) + uint32_t(n)) * 2u : kOutside;
+        return c;
+    };
+    auto advance = [&](Cursor& c) {
+        ++c.k;
+        --c.left;
+        if (P::TURN && c.k == blocks) c.k = 0;
+    };
     struct Source {
         __amdgpu_buffer_rsrc_t r, up;      // up: gated
         uint32_t off, group;
     };
-    // Block of k of step s: the steps past the last one are all zeros.
-    auto block_of = [&](const Base& b, int s) {
-        const int k = s + b.turn;
-        return P::TURN && k >= blocks ? k - blocks : k;
-    };
-    auto rows_source = [&](const uint8_t* base, const uint8_t* up, int64_t bytes, const Base& b, int s) {
-        const int k0 = block_of(b, s) * kBK;
-        const int left = s < blocks ? row_bytes - k0 : 0;
+    // Rows from block k on.  A lane's chunk of the last block may lie behind the row's end.
+    const int chunk_end = row_bytes - lchunk * 16;
+    auto rows_source = [&](const Cursor& c, const uint8_t* base, const uint8_t* up, int bytes) {
+        const int k0 = c.k * kBK;
+        const int use = c.left > 0 && bytes > k0 ? bytes - k0 : 0;
         int off = off0;
         hide(off);          // or every load's offset would take a register of its own
-        const int64_t use = left > 0 && bytes > k0 ? bytes - k0 : 0;
-        Source c;
-        c.r = buffer_rsrc(const_cast<uint8_t*>(base) + (use ? k0 : 0), use);
-        c.up = buffer_rsrc(const_cast<uint8_t*>(up) + (use ? k0 : 0), use);
-        c.off = uint32_t(off) | (lchunk * 16 >= left ? kOutside : 0);
-        c.group = uint32_t(row_bytes) * 32u;
-        return c;
+        return Source{buffer_rsrc(const_cast<uint8_t*>(base) + k0, use),
+                      buffer_rsrc(const_cast<uint8_t*>(up) + k0, use),
+                      k0 < chunk_end ? uint32_t(off) : kOutside, uint32_t(row_bytes) * 32u};
     };
-    auto weights_source = [&](const Base& b, int s) {
-        if (!TRANS) return rows_source(b.w, GATED ? b.w + int64_t(N) * row_bytes : b.w, b.wbytes, b, s);
-        const int k0 = block_of(b, s) * (kBK / 2);
-        const int left = s < blocks && b.wbytes ? p.K - k0 : 0;
-        int n = b.col0 + tchunk * 8;
-        hide(n);
-        const int64_t rows = left <= 0 ? 0 : left < kBK / 2 ? left : kBK / 2;
-        Source c;
-        c.r = c.up = buffer_rsrc(const_cast<uint8_t*>(b.w) + (rows ? int64_t(k0) * N * 2 : 0), rows * N * 2);
-        c.off = n < N ? (uint32_t(trow) * uint32_t(N) + uint32_t(n)) * 2u : kOutside;
-        c.group = uint32_t(N) * uint32_t(kRowsPerLoad * 8);
-        return c;
+    auto weights_source = [&](const Cursor& c) {
+        if (!TRANS)
+            return rows_source(c, c.w, GATED ? c.w + int64_t(N) * row_bytes : c.w, c.wbytes);
+        const int k0 = c.k * (kBK / 2);
+        const int rows = p.K - k0 < kBK / 2 ? p.K - k0 : kBK / 2;
+        int off = int(c.woff);
+        hide(off);
+        const __amdgpu_buffer_rsrc_t r = buffer_rsrc(
+            const_cast<uint8_t*>(c.w) + int64_t(k0) * N * 2, c.left > 0 ? rows * c.wbytes : 0);
+        return Source{r, r, uint32_t(off), uint32_t(N) * uint32_t(kRowsPerLoad * 8)};
     };
-    auto tokens_source = [&](const Base& b, int s) { return rows_source(b.x, b.x, b.xbytes, b, s); };
+    auto tokens_source = [&](const Cursor& c) { return rows_source(c, c.x, c.x, c.xbytes); };
     // load i of the weights: rows 32 i on, or gated groups of 32 rows that alternate
     // between gate and up
     auto issue_w = [&](const Source& c, uint8_t* to, int i) {
@@ -222,23 +216,26 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
             f.w[m] = load16(ws + woff + m * 32 * kBK + foff[q]);
         }
     };
+    constexpr int kSlots = FN * FM;
     typename T::Acc acc[FN][FM];
-    // FN x FM matrix instructions on `f`, between them the reads of the next quarter
-    // (quarter q of stages ws and xs) and the loads [first, last) of `src` into `to`.
+    // FN x FM matrix instructions on `f` (half: the first half, -1, or the second, 1), in
+    // the first half the reads of the next quarter (quarter q of stages ws and xs), and
+    // throughout the loads [first, last) of `src` into `to`.
     // Each matrix instruction is held in its place: the compiler would gather them
     // otherwise, and run out of registers.  The stages are named restrict: it would
     // wait for every load into LDS before a transposing read otherwise.
     auto multiply = [&](const Quarter& f, uint8_t* __restrict__ ws, uint8_t* __restrict__ xs, int q,
                         Quarter& next, const Source& src, uint8_t* __restrict__ to, bool weights,
-                        int first, int last) {
-        constexpr int kSlots = FN * FM;
+                        int first, int last, int half) {
+        constexpr int kEarly = (kSlots + 1) / 2;
 #pragma unroll
-        for (int n = 0; n < kSlots; ++n) {
+        for (int n = half > 0 ? kSlots / 2 : 0; n < (half < 0 ? kSlots / 2 : kSlots); ++n) {
             const int i = n / FM, j = n % FM;
             acc[i][j] = T::mfma(f.w[i], f.x[j], acc[i][j]);
             pin(acc[i][j]);
 #pragma unroll
-            for (int r = n * kReads / kSlots; r < (n + 1) * kReads / kSlots; ++r) read(ws, xs, q, next, r);
+            for (int r = n * kReads / kEarly; r < (n + 1) * kReads / kEarly && r < kReads; ++r)
+                read(ws, xs, q, next, r);
 #pragma unroll
             for (int r = first + n * (last - first) / kSlots;
                  r < first + (n + 1) * (last - first) / kSlots; ++r) {
@@ -253,14 +250,15 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     if (t.rows.expert < 0) return;
     // a tile's loads reach into the next one only
     const int steps = blocks > STAGES - 1 ? blocks : STAGES - 1;
-    Base cur = base_of(t);
+    Cursor cursor = start(t);
 #pragma unroll
     for (int d = 0; d < STAGES - 1; ++d) {
-        const Source w = weights_source(cur, d), x = tokens_source(cur, d);
+        const Source w = weights_source(cursor), x = tokens_source(cursor);
 #pragma unroll
         for (int i = 0; i < kWLoads; ++i) issue_w(w, lds + d * kWStage, i);
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) issue_x(x, xlds + d * kXStage, i);
+        advance(cursor);
     }
     wait_and_barrier<(STAGES - 2) * kStepLoads>();
     Quarter f0, f1;
@@ -270,7 +268,8 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
 
     for (int turn = 1;; ++turn) {
         const GemmTile tnext = tiles.at(p, TM, turn);
-        const Base next = base_of(tnext);
+        if (steps == STAGES - 1) cursor = start(tnext);
+        Source w = weights_source(cursor);
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -281,16 +280,18 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
             const int wnext = wslot == STAGES - 1 ? 0 : wslot + 1;
             const int wlast = wslot == 0 ? STAGES - 1 : wslot - 1;
             const int xnext = xslot == STAGES - 2 ? 0 : xslot + 1;
-            const bool over = s + STAGES - 1 >= steps;
-            const int ahead = over ? s + STAGES - 1 - steps : s + STAGES - 1;
-            const Base& from = over ? next : cur;
             uint8_t* const ws = lds + wslot * kWStage;
             uint8_t* const xs = xlds + xslot * kXStage;
-            const Source w = weights_source(from, ahead);
             uint8_t* const to = lds + wlast * kWStage;
-            multiply(f0, ws, xs, 1, f1, w, to, true, 0, kWLoads / 2);
-            multiply(f1, ws, xs, 2, f0, w, to, true, kWLoads / 2, kWLoads);
-            multiply(f0, ws, xs, 3, f1, w, to, true, 0, 0);
+            multiply(f0, ws, xs, 1, f1, w, to, true, 0, kWLoads / 2, 0);
+            multiply(f1, ws, xs, 2, f0, w, to, true, kWLoads / 2, kWLoads, 0);
+            // what the next loads need is worked out between matrix instructions: ahead of
+            // a quarter it would leave the matrix unit idle
+            multiply(f0, ws, xs, 3, f1, w, to, true, 0, 0, -1);
+            const Source x = tokens_source(cursor);
+            advance(cursor);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(f0, ws, xs, 3, f1, w, to, true, 0, 0, 1);
             // newer than the next step's loads: those of STAGES - 3 steps, this step's
             // weights, and in a tile's first step the last tile's stores
             constexpr int kNewer = (STAGES - 3) * kStepLoads + kWLoads;
@@ -298,8 +299,14 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
             if (s == 0 && turn > 1) wait_and_barrier<kAfterStores>();
             else wait_and_barrier<kNewer>();
             __builtin_amdgcn_sched_barrier(0);
-            const Source x = tokens_source(from, ahead);
-            multiply(f1, lds + wnext * kWStage, xlds + xnext * kXStage, 0, f0, x, xs, false, 0, kXLoads);
+            uint8_t* const wsn = lds + wnext * kWStage;
+            uint8_t* const xsn = xlds + xnext * kXStage;
+            multiply(f1, wsn, xsn, 0, f0, x, xs, false, 0, kXLoads, -1);
+            // the last STAGES - 1 steps of a tile load the first ones of the next
+            if (s + STAGES == steps) cursor = start(tnext);
+            w = weights_source(cursor);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(f1, wsn, xsn, 0, f0, x, xs, false, 0, kXLoads, 1);
             wslot = wnext;
             xslot = xnext;
         }
@@ -398,7 +405,6 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
         if (tnext.rows.expert < 0) break;
         wait_and_barrier<63>();     // the scratch has been read before the next loads into it
         t = tnext;
-        cur = next;
     }
     wait_and_barrier<0>();          // no load into LDS outlives the workgroup
 }
