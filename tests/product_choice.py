@@ -1,0 +1,90 @@
+"""The library's choice of kernel for the bf16 and int8 products (csrc/experts/expert_choice.h), compiled for
+the host: tests use it to know that their sizes reach the kernel they are for."""
+import ctypes
+import functools
+import os
+import subprocess
+import tempfile
+
+from expert_choice import CUS, HEADER
+
+KERNELS = ["256x256", "256x128", "128x128", "256x64", "128x64", "narrow 64x64", "narrow 32x64", "narrow 32x32"]
+TOKENS = {"256x128": 128, "128x128": 128, "256x64": 64, "128x64": 64}      # of those that may pass the caches
+
+SHIM = f"""
+#include "{HEADER}"
+extern "C" int product(long long S, long long N, long long row_bytes, long long E, int gated, long long cus) {{
+    return ep::choose_product(S, N, row_bytes, E, gated != 0, cus);
+}}
+extern "C" int past(long long S, long long N, long long row_bytes, long long E, int gated, long long line,
+                    long long tokens) {{
+    return ep::product_past_caches(S, N, row_bytes, E, gated != 0, line, tokens);
+}}
+extern "C" int tile(int kernel, int tokens) {{
+    return tokens ? ep::product_tile(kernel).tokens : ep::product_tile(kernel).weights;
+}}
+"""
+
+
+@functools.lru_cache(maxsize=None)
+def _lib():
+    with tempfile.TemporaryDirectory() as d:
+        src, lib = os.path.join(d, "shim.cpp"), os.path.join(d, "shim.so")
+        with open(src, "w") as f:
+            f.write(SHIM)
+        subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wall", "-Werror", "-o", lib, src],
+                       check=True)
+        h = ctypes.CDLL(lib)
+    h.product.argtypes = [ctypes.c_longlong] * 4 + [ctypes.c_int, ctypes.c_longlong]
+    h.past.argtypes = [ctypes.c_longlong] * 4 + [ctypes.c_int] + [ctypes.c_longlong] * 2
+    return h
+
+
+def product(S, N, K, E, bytes_=2, gated=False, transposed=False):
+    """(kernel's name, whether its weights go past the caches).  N: columns of the result."""
+    name = KERNELS[_lib().product(S, N, K * bytes_, E, int(gated), CUS)]
+    line = N * bytes_ if transposed else K * bytes_
+    past = name in TOKENS and bool(_lib().past(S, N, K * bytes_, E, int(gated), line, TOKENS[name]))
+    return name, past
+
+
+def tile(name):
+    k = KERNELS.index(name)
+    return _lib().tile(k, 0), _lib().tile(k, 1)
+
+
+# Segments (rows of each expert), columns and lengths of k that between them reach every kernel
+_SEGMENTS = ([5, 9, 3], [1, 0, 2], [1000, 0, 1], [500, 0, 400, 3], [250] * 4, [1] * 8 + [0] * 8, [10] * 8, [64] * 8,
+             [96] * 8, [100, 0, 90, 1], [60] * 16, [11] * 15 + [100], [128] * 16, [45] * 18, [130] * 30,
+             [3000, 0, 4000, 1, 2999], [4] * 64, [300] * 70, [2] * 100)
+_COLUMNS = (80, 144, 208, 264, 272, 520, 528, 784, 1040, 1408, 2064, 2816, 4096)
+_LENGTHS = (80, 144, 272, 336, 400, 528, 1040, 2064, 4096, 7168)
+
+
+@functools.lru_cache(maxsize=None)
+def case(name, past, bytes_, kind, behind=0):
+    """The least case that reaches a kernel: (rows of each expert, columns, K); None if there is none."""
+    best = None
+    for counts in _SEGMENTS:
+        for N in _COLUMNS:
+            for K in _LENGTHS:
+                E, S = len(counts), sum(counts) + behind
+                if bytes_ == 1 and (N % 16 or K % 16):
+                    continue
+                cost = E * N * K * (2 if kind == "gated" else 1) + S * (N + K)
+                if best is not None and cost >= best[0]:
+                    continue
+                if product(S, N, K, E, bytes_, kind == "gated", kind == "transposed") == (name, past):
+                    best = (cost, (counts, N, K))
+    return best[1] if best else None
+
+
+def cases():
+    """(bytes, kind, kernel, past the caches) of everything that a call can launch."""
+    return [(b, kind, name, past) for b in (2, 1) for kind in ("plain", "transposed", "gated")
+            if (b, kind) != (1, "transposed") for name in KERNELS for past in (False, True)
+            if not past or name in TOKENS]
+
+
+def label(c):
+    return f"{'bf16' if c[0] == 2 else 'int8'} {c[1]} {c[2]}{' past' if c[3] else ''}".replace(" ", "-")
