@@ -1,10 +1,17 @@
 // expert_choice.h -- which kernel a grouped product or a weight gradient takes.
-// Host rules on sizes alone, in a header of their own so that a test can ask
-// which kernel its sizes reach.
+// Rules on sizes (and, for the bf16 and int8 products' tiles, on how the rows fall on the
+// experts), in a header of their own so that a test can ask which kernel its sizes reach.
 #pragma once
 
 #include <math.h>
 #include <stdint.h>
+
+#if defined(__HIPCC__)
+#include <hip/hip_runtime.h>
+#define EP_BOTH __host__ __device__ inline
+#else
+#define EP_BOTH inline
+#endif
 
 namespace ep {
 
@@ -87,93 +94,122 @@ enum ProductKernel {
     kNarrow32x32,
     kProductKernels,
 };
+constexpr int kProductTiles = kNarrow64x64;      // the persistent ones come first
+constexpr float kLookUs = 1.0f;                  // and look at the segments before
 
-// What a tile takes on MI355X, us: `tile`, and `step` for each 128 bytes of k, of the
-// tiles that the CUs work on at once.  Fitted to 4455 measured sizes (1 to 64 experts of
-// 1 to 2500 rows on average, even, as even picks fall or by a Zipf law, 64 to 8192 weight
-// rows, 128 to 8192 values of k, bf16 either way round, gated and int8, weights from
-// memory): the kernel chosen by them takes 2% longer than the best one on average (3% by the
-// Zipf law), 20% at the 97th percentile, 2.4 times at the worst (a Zipf law, which sizes
-// do not tell).  Without the 256 x 256 tiles the best of the others takes 2% longer on average
-// and 50% at most, without 256 x 128 1% and 38%, 128 x 128 1% and 46%, 256 x 64 0.5% and
-// 17%, 128 x 64 1.5% and 38%, without the narrow ones 1.6, 1 and 7%, and up to 72%.  For
-// instance, us (bf16, weights from memory):
+// What a tile takes on MI355X, us: `tile`, and `step` for each 128 bytes of k.  Fitted to 4970
+// measured sizes (1 to 64 experts of 1 to 2500 rows on average, even, as even picks
+// fall or by a Zipf law, 64 to 8192 weight rows, 128 to 8192 values of k, bf16 either way
+// round, gated and int8, weights from memory): what is chosen by them takes 0.9% longer than
+// the best on average (1.3% by the Zipf law), 9% at the 97th percentile, twice as long at the worst
+// (a few rows on fewer experts than they could fall on).  With the row tiles estimated
+// from sizes, and not counted in the segments, it was 2.2%, 20% and 2 times.  What the best
+// of the others takes without one of them, on average and at the worst: 256 x 256 1.8% and
+// 59%, 256 x 128 1.3% and 38%, 128 x 128 0.9% and 54%, 256 x 64 0.6% and 27%, 128 x 64
+// 1.8% and 36%, narrow 64 x 64 1.2% and 57%, 32 x 64 0.9% and 40%, 32 x 32 6.3% and 57%.
+// For instance, us (bf16, weights from memory):
 //                                          256x256 256x128 128x128 256x64 128x64 32x32
-//   8 experts x 4096 x 7168, 8 rows each                             93     70     77
+//   8 experts x 4096 x 7168, 8 rows each                     75      93     70     77
 //   16 x 2816 x 4096, 64                                     79      61     77    131
 //   16 x 2816 x 4096, 128                    89      67      99
-//   8 x 4096 x 7168, 500                    186     221     257
-//   1 x 4096 x 4096, 1024                    78      54      43      48
+//   8 x 4096 x 7168, 500                    173     217     257
+//   1 x 4096 x 4096, 1024                    78      54      39      48
 //   4 x 2048 x 4096, 8                                               44     28     14
 //   1 x 4096 x 7168, 8                                               78     46     16
 struct ProductTile {
     int weights, tokens;
-    int per_cu;              // workgroups a CU; 0: not persistent, about one at a time
-    double step, tile;
+    float step, tile;
 };
-inline const ProductTile& product_tile(int kernel)
+EP_BOTH ProductTile product_tile(int kernel)
 {
-    static const ProductTile tiles[kProductKernels] = {
-        {256, 256, 1, 1.355, 7.7}, {256, 128, 1, 0.94, 3.7}, {128, 128, 2, 1.455, 1.27},
-        {256, 64, 1, 0.80, 2.1},   {128, 64, 1, 0.41, 1.57}, {64, 64, 0, 0.385, 1.6},
-        {32, 64, 0, 0.34, 1.73},   {32, 32, 0, 0.34, 1.68},
+    constexpr ProductTile tiles[kProductKernels] = {
+        {256, 256, 1.25f, 4.2f}, {256, 128, 0.89f, 1.85f}, {128, 128, 0.53f, 2.0f},
+        {256, 64, 0.795f, 1.1f}, {128, 64, 0.395f, 1.1f},  {64, 64, 0.39f, 2.15f},
+        {32, 64, 0.377f, 1.95f}, {32, 32, 0.363f, 1.95f},
     };
     return tiles[kernel];
 }
-constexpr double kStepAlone128x128 = 0.80;      // one workgroup on each CU
-constexpr double kBytesPerUs = 6.6e6;
-
-// N: columns of the result; row_bytes: of a row of k; gated: 2 N weight rows.  At
-// most S experts have rows; picks that fall evenly give them their square root more
-// or less, and the fuller ones count.  Where memory bounds several alike, the largest
-// tile.
-inline ProductKernel choose_product(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bool gated,
-                                    int64_t cus)
+// The same for all tiles, on so many CUs at once.
+EP_BOTH float product_us(int kernel, float tiles, int blocks, int cus)
 {
-    const double used = double(S < E ? S : E), rows = double(S) / used;
-    const double blocks = double((row_bytes + 127) / 128);
-    const double bytes = double(row_bytes) * (used * double(gated ? 2 * N : N) + double(S)) +
-                         2.0 * double(S) * double(N);
-    const double slots = double(cus > 8 ? cus / 8 : 1);      // CUs of an XCD
-    ProductKernel best = kProduct256x256;
-    double least = 0.0;
-    for (int k = 0; k < kProductKernels; ++k) {
-        const ProductTile& t = product_tile(k);
-        const int64_t columns = gated ? t.weights / 2 : t.weights;
-        double row_tiles = used * ceil((rows + sqrt(rows)) / t.tokens);
-        if (row_tiles > double(S)) row_tiles = double(S);
-        const double tiles = ceil(row_tiles * double((N + columns - 1) / columns));
-        double rounds, step = t.step;
-        if (t.per_cu == 0) {
-            rounds = tiles / (8.0 * slots);
-            if (rounds < 1.0) rounds = 1.0;
-        } else {
-            const double one = ceil(ceil(tiles / 8.0) / slots);
-            rounds = ceil(one / t.per_cu);
-            if (t.per_cu > 1 && one <= 1.0) step = kStepAlone128x128;
-        }
-        double us = rounds * (t.tile + blocks * step);
-        if (us < bytes / kBytesPerUs) us = bytes / kBytesPerUs;
+    const ProductTile t = product_tile(kernel);
+    float rounds = tiles / float(cus);
+    if (kernel < kProductTiles) {
+        // each XCD has an eighth of the tiles, and its workgroups take them in turn
+        const int share = (int(tiles) + 7) / 8, slots = cus / 8;
+        rounds = float((share + slots - 1) / slots);
+    } else if (rounds < 1.0f) {
+        rounds = 1.0f;
+    }
+    return rounds * (t.tile + float(blocks) * t.step);
+}
+
+// The persistent tile for segments that make so many row tiles of 64, 128 and 256
+// rows, n tiles of `weights` (gated: half as many columns) each.
+EP_BOTH int choose_product_tile(int tiles64, int tiles128, int tiles256, int N, int blocks, bool gated,
+                                int cus)
+{
+    int best = 0;
+    float least = 0.0f;
+    for (int k = 0; k < kProductTiles; ++k) {
+        const ProductTile t = product_tile(k);
+        const int columns = gated ? t.weights / 2 : t.weights;
+        const int rows = t.tokens == 64 ? tiles64 : t.tokens == 128 ? tiles128 : tiles256;
+        const float us = product_us(k, float(rows * ((N + columns - 1) / columns)), blocks, cus);
         if (k == 0 || us < least) {
             least = us;
-            best = ProductKernel(k);
+            best = k;
         }
     }
     return best;
 }
 
-// Whether tiles of so many tokens read the weights past the caches: each of them once
-// (no more rows than one tile holds), more than the caches keep until the next call, in
-// whole lines.  Past / through the caches, weights from memory: 0.89 to 0.96 with 64 MB and
-// more, 0.87 to 0.98 with less (but 33 MB that the last call left there would take 15 us
-// instead of 11); with more rows than a tile holds 1.0 to 1.2; with rows of k that do not
-// begin on lines 1.0 to 1.15.
-inline bool product_past_caches(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bool gated,
-                                int64_t line_bytes, int64_t tokens)
+// Whether such a tile reads the weights past the caches: where each of them is read once.
+// Past / through the caches, weights from memory: 0.89 to 0.96 with 64 MB and more, 0.87 to 0.98
+// with less (but 33 MB that the last call left there would take 15 us instead of 11); with
+// more rows than a tile holds 1.0 to 1.2; with rows of k that do not begin on lines 1.0 to
+// 1.15.
+EP_BOTH bool product_past_caches(int row_tiles, int used, bool whole_lines)
 {
-    const int64_t used = S < E ? S : E;
-    return S <= tokens * used && (gated ? 2 : 1) * E * N * row_bytes > (int64_t(64) << 20) &&
-           line_bytes % 128 == 0;
+    return whole_lines && row_tiles <= used;
+}
+
+// Whether a call takes the persistent kernel, which looks at the segments itself, or a
+// narrow one.  The host knows sizes only: rows spread evenly between 0.4 and 1.6 of the
+// average, and their square root more or less.
+// N: columns of the result; row_bytes: of a row of k; gated: 2 N weight rows.
+inline int choose_product(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bool gated, int64_t cus)
+{
+    const double used = double(S < E ? S : E), rows = double(S) / used;
+    const int blocks = int((row_bytes + 127) / 128);
+    auto upto = [](double x) {               // integral of ceil from 0
+        return x <= 0.0 ? 0.0 : floor(x) * (floor(x) + 1.0) / 2.0 + ceil(x) * (x - floor(x));
+    };
+    int best = 0;
+    float least = 0.0f;
+    for (int k = 0; k < kProductKernels; ++k) {
+        const ProductTile t = product_tile(k);
+        const int64_t columns = gated ? t.weights / 2 : t.weights;
+        const double high = (1.6 * rows + sqrt(rows)) / t.tokens;
+        const double low = fmax((0.4 * rows - sqrt(rows)) / t.tokens, 0.0);
+        double each = used == 1.0 ? ceil(rows / t.tokens) : (upto(high) - upto(low)) / (high - low);
+        if (each < 1.0) each = 1.0;
+        const double tiles = ceil(fmin(used * each, double(S)) * double((N + columns - 1) / columns));
+        const float us = product_us(k, float(fmin(tiles, 1e9)), blocks, int(cus > 8 ? cus : 8)) +
+                         (k < kProductTiles ? kLookUs : 0.0f);
+        if (k == 0 || us < least) {
+            least = us;
+            best = k < kProductTiles ? 0 : k;
+        }
+    }
+    return best;
+}
+
+// Whether the weights' rows begin on lines and are more than the caches keep until the
+// next call.
+inline bool product_whole_lines(int64_t N, int64_t row_bytes, int64_t E, bool gated, int64_t line_bytes)
+{
+    return (gated ? 2 : 1) * E * N * row_bytes > (int64_t(64) << 20) && line_bytes % 128 == 0;
 }
 
 // ------------------------------------------------------------- weight gradients

@@ -22,6 +22,7 @@
 // last quarter, into the stage that s itself has just left.
 #pragma once
 
+#include "expert_choice.h"
 #include "expert_tiles.h"
 
 namespace ep {
@@ -75,7 +76,6 @@ struct ProductShape {
     static constexpr int TN = 32 * FN * WN, TM = 32 * FM * (4 / WN);
     static constexpr int kColumns = GATED ? TN / 2 : TN;      // of y or h
     static constexpr int kLds = (STAGES * TN + (STAGES - 1) * TM) * 128;
-    static constexpr int kOccupancy = kLds > 80 * 1024 ? 1 : kLds > 160 * 1024 / 3 ? 2 : 3;
     // stores of one tile that every wave issues
     static constexpr int kStores = (KIND == kGated ? 1 : KIND == kGatedSaved ? 3 : 2) * FN * FM;
     static constexpr bool kStoreNt = TN == 256 && TM == 256;
@@ -83,8 +83,15 @@ struct ProductShape {
     static_assert(!TRANS || TN >= 128, "a row of a transposed stage has four units at least");
 };
 
+// What was found in the segments: their row tiles of the shape's size, and of up to 64
+// experts the one of each lane.
+struct Segments {
+    int row_tiles, begin, end;
+};
+
+// The workgroup's share of the tiles of shape P.
 template <class P>
-__global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(ProductArgs p)
+__device__ __forceinline__ void product_tiles(const ProductArgs& p, const Segments& segments, uint8_t* lds)
 {
     typedef typename P::T T;
     constexpr int FN = P::FN, FM = P::FM, TN = P::TN, TM = P::TM, STAGES = P::STAGES;
@@ -93,7 +100,6 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     constexpr int kWStage = TN * kBK, kXStage = TM * kBK;
     constexpr int kWLoads = TN / 32, kXLoads = TM / 32;  // of 16 bytes a thread
     constexpr int kStepLoads = kWLoads + kXLoads;
-    __shared__ __attribute__((aligned(256))) uint8_t lds[P::kLds];
     uint8_t* const xlds = lds + STAGES * kWStage;
 
     const int lane = lane_id();
@@ -101,7 +107,8 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     const int wn = wave % P::WN, wm = wave / P::WN;
     const int N = p.N, row_bytes = p.K * T::kBytes;
     const int blocks = (row_bytes + kBK - 1) / kBK;
-    const GemmTiles tiles(p, TM, (N + P::kColumns - 1) / P::kColumns);
+    const GemmTiles tiles(TM, (N + P::kColumns - 1) / P::kColumns, segments.row_tiles, segments.begin,
+                          segments.end);
 
     // LDS image of rows of 128 bytes: chunk c of 16 at slot c ^ (row / 2 % 8), so that
     // the 16 lanes that read one chunk of 16 rows touch every bank once.  A load
@@ -382,14 +389,25 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
             if constexpr (T::kScaled) return float(acc[i][j][c]) * wscale[i][c / 4][c % 4] * token[j];
             else return float(acc[i][j][c]);
         };
+        // The accumulators stay where they are until their turn: all at once they would
+        // take registers that spill.
+        auto take = [&](int j) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < FN; ++i) pin(acc[i][j]);
+        };
         if constexpr (!GATED) {
             const __amdgpu_buffer_rsrc_t r = buffer_rsrc(p.y + row0 * N, int64_t(rows) * N * 2);
 #pragma unroll
-            for (int j = 0; j < FM; ++j) put([&](int i, int c) { return value(i, j, c); }, r, N, 0, j);
+            for (int j = 0; j < FM; ++j) {
+                take(j);
+                put([&](int i, int c) { return value(i, j, c); }, r, N, 0, j);
+            }
         } else {
             const __amdgpu_buffer_rsrc_t hr = buffer_rsrc(p.h + row0 * N, int64_t(rows) * N * 2);
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
+                take(j);
                 if constexpr (P::KIND == kGatedSaved) {
                     const __amdgpu_buffer_rsrc_t yr =
                         buffer_rsrc(p.y + row0 * 2 * N, int64_t(rows) * N * 4);
@@ -409,14 +427,87 @@ __global__ __launch_bounds__(256, P::kOccupancy) void expert_product_kernel(Prod
     wait_and_barrier<0>();          // no load into LDS outlives the workgroup
 }
 
-template <class P>
-hipError_t launch_product(ProductArgs p, hipStream_t s)
+// Sum over the wave by row moves: the shuffles of wave_inclusive_sum would have the
+// compiler keep their addresses, and spill them, for the tiles' own.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_moved(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_sum(int v) {
+    v = add_moved<0x111, 0xF>(v);       // from 1, 2, 4 and 8 lanes below in a row of 16
+    v = add_moved<0x112, 0xF>(v);
+    v = add_moved<0x114, 0xF>(v);
+    v = add_moved<0x118, 0xF>(v);
+    v = add_moved<0x142, 0xA>(v);       // a row's last lane to the odd row above it
+    v = add_moved<0x143, 0xC>(v);       // the lower half's to the upper half
+    return __builtin_amdgcn_readlane(v, kWave - 1);
+}
+
+// Which shape: by the row tiles that the segments make of each size, counted here, since
+// sizes do not tell how the rows fall on the experts (choose_product_tile).  One
+// workgroup a CU.  whole_lines: the weights' rows begin on lines and are more than the
+// caches keep.
+template <class T, ProductKind KIND>
+__global__ __launch_bounds__(256, 1) void expert_product_kernel(ProductArgs p, int whole_lines)
 {
-    uint32_t grid = gemm_tiles(p, P::TM, P::kColumns);
-    if (!grid) return hipErrorInvalidConfiguration;
-    const uint32_t most = device_cu_count() / 8 * 8 * P::kOccupancy;
-    grid = grid < most || most == 0 ? grid : most;
-    EP_LAUNCH((expert_product_kernel<P>), dim3(grid), dim3(256), 0, s, p);
+    __shared__ __attribute__((aligned(256))) uint8_t lds[160 * 1024];
+    int used = 0, tiles[3] = {0, 0, 0};            // of 64, 128 and 256 rows
+    Segments found = {0, 0, 0};
+    for (int e = int(threadIdx.x) % kWave; e < p.E; e += kWave) {
+        segment_of(p.offsets, e, p.S, found.begin, found.end);
+        const int rows = found.end - found.begin;
+        used += rows > 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            tiles[i] += (rows + (64 << i) - 1) >> (6 + i);
+            tiles[i] = tiles[i] < (1 << 24) ? tiles[i] : (1 << 24);      // 64 lanes stay below 2^31
+        }
+    }
+    used = wave_sum(used);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        // segments that do not overlap cannot pass the limit; others are cut there
+        const int limit = (p.S >> (6 + i)) + (p.E < p.S ? p.E : p.S);
+        tiles[i] = wave_sum(tiles[i]);
+        tiles[i] = tiles[i] < limit ? tiles[i] : limit;
+    }
+    const int blocks = (p.K * T::kBytes + 127) / 128;
+    const int kernel = choose_product_tile(tiles[0], tiles[1], tiles[2], p.N, blocks, KIND >= kGated,
+                                           int(gridDim.x));
+    const int tokens = product_tile(kernel).tokens;
+    found.row_tiles = tokens == 64 ? tiles[0] : tokens == 128 ? tiles[1] : tiles[2];
+    const bool past = product_past_caches(found.row_tiles, used, whole_lines != 0);
+    switch (kernel) {
+        case kProduct256x256: product_tiles<ProductShape<T, KIND, 4, 4, 2, 3, false, false>>(p, found, lds); break;
+        case kProduct256x128:
+            if (past) product_tiles<ProductShape<T, KIND, 4, 2, 2, 3, true, true>>(p, found, lds);
+            else product_tiles<ProductShape<T, KIND, 4, 2, 2, 3, true, false>>(p, found, lds);
+            break;
+        case kProduct128x128:
+            if (past) product_tiles<ProductShape<T, KIND, 2, 2, 2, 4, true, true>>(p, found, lds);
+            else product_tiles<ProductShape<T, KIND, 2, 2, 2, 4, true, false>>(p, found, lds);
+            break;
+        case kProduct256x64:
+            if (past) product_tiles<ProductShape<T, KIND, 2, 2, 4, 3, true, true>>(p, found, lds);
+            else product_tiles<ProductShape<T, KIND, 2, 2, 4, 3, true, false>>(p, found, lds);
+            break;
+        default:
+            if (past) product_tiles<ProductShape<T, KIND, 2, 1, 2, 4, true, true>>(p, found, lds);
+            else product_tiles<ProductShape<T, KIND, 2, 1, 2, 4, true, false>>(p, found, lds);
+    }
+}
+
+template <class T, ProductKind KIND>
+hipError_t launch_product(const ProductArgs& p, hipStream_t s)
+{
+    const int64_t row_bytes = int64_t(p.K) * T::kBytes;
+    const int64_t line_bytes = KIND == kTransposed ? int64_t(p.N) * T::kBytes : row_bytes;
+    const bool whole = product_whole_lines(p.N, row_bytes, p.E, KIND >= kGated, line_bytes);
+    // as many tiles as the smallest shape can make
+    ProductArgs least = p;
+    if (!gemm_tiles(least, 64, KIND >= kGated ? 64 : 128)) return hipErrorInvalidConfiguration;
+    const uint32_t cus = device_cu_count() / 8 * 8;
+    EP_LAUNCH((expert_product_kernel<T, KIND>), dim3(cus ? cus : 8), dim3(256), 0, s, p, int(whole));
     return hipGetLastError();
 }
 

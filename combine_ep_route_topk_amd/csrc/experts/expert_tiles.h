@@ -35,6 +35,15 @@ struct GemmTiles {
             mt = count_row_tiles(p.offsets, p.E, p.S, TM, p.max_tiles);
         }
     }
+    // Of segments that were looked at before: lane e's is [begin, past) (up to 64
+    // experts), and they make `row_tiles` row tiles.
+    __device__ __forceinline__ GemmTiles(int TM, int n_tiles, int row_tiles, int begin, int past)
+        : mt(row_tiles), nt(n_tiles), b(begin), end(past)
+    {
+        int tiles = (end - b + TM - 1) / TM;
+        tiles = tiles < (1 << 24) ? tiles : (1 << 24);
+        upto = wave_inclusive_sum(tiles);
+    }
     // The workgroup's tile number `turn`, of those of its XCD slot / 8 apart by
     // gridDim / 8.
     template <class Args>

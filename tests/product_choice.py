@@ -9,19 +9,22 @@ import tempfile
 from expert_choice import CUS, HEADER
 
 KERNELS = ["256x256", "256x128", "128x128", "256x64", "128x64", "narrow 64x64", "narrow 32x64", "narrow 32x32"]
-TOKENS = {"256x128": 128, "128x128": 128, "256x64": 64, "128x64": 64}      # of those that may pass the caches
+# tokens of the tiles that may read the weights past the caches
+TOKENS = {"256x128": 128, "128x128": 128, "256x64": 64, "128x64": 64}
 
 SHIM = f"""
 #include "{HEADER}"
 extern "C" int product(long long S, long long N, long long row_bytes, long long E, int gated, long long cus) {{
     return ep::choose_product(S, N, row_bytes, E, gated != 0, cus);
 }}
-extern "C" int past(long long S, long long N, long long row_bytes, long long E, int gated, long long line,
-                    long long tokens) {{
-    return ep::product_past_caches(S, N, row_bytes, E, gated != 0, line, tokens);
+extern "C" int tile(int t64, int t128, int t256, int N, int blocks, int gated, int cus) {{
+    return ep::choose_product_tile(t64, t128, t256, N, blocks, gated != 0, cus);
 }}
-extern "C" int tile(int kernel, int tokens) {{
-    return tokens ? ep::product_tile(kernel).tokens : ep::product_tile(kernel).weights;
+extern "C" int whole(long long N, long long row_bytes, long long E, int gated, long long line) {{
+    return ep::product_whole_lines(N, row_bytes, E, gated != 0, line);
+}}
+extern "C" int past(int row_tiles, int used, int whole) {{
+    return ep::product_past_caches(row_tiles, used, whole != 0);
 }}
 """
 
@@ -36,29 +39,30 @@ def _lib():
                        check=True)
         h = ctypes.CDLL(lib)
     h.product.argtypes = [ctypes.c_longlong] * 4 + [ctypes.c_int, ctypes.c_longlong]
-    h.past.argtypes = [ctypes.c_longlong] * 4 + [ctypes.c_int] + [ctypes.c_longlong] * 2
+    h.whole.argtypes = [ctypes.c_longlong] * 3 + [ctypes.c_int, ctypes.c_longlong]
     return h
 
 
-def product(S, N, K, E, bytes_=2, gated=False, transposed=False):
-    """(kernel's name, whether its weights go past the caches).  N: columns of the result."""
-    name = KERNELS[_lib().product(S, N, K * bytes_, E, int(gated), CUS)]
-    line = N * bytes_ if transposed else K * bytes_
-    past = name in TOKENS and bool(_lib().past(S, N, K * bytes_, E, int(gated), line, TOKENS[name]))
-    return name, past
-
-
-def tile(name):
-    k = KERNELS.index(name)
-    return _lib().tile(k, 0), _lib().tile(k, 1)
+def product(counts, N, K, bytes_=2, kind="plain", behind=0):
+    """(kernel's name, whether its weights go past the caches) for so many rows of each expert and `behind` of
+    none.  N: columns of the result."""
+    h, E, S, gated = _lib(), len(counts), sum(counts) + behind, int(kind == "gated")
+    k = h.product(S, N, K * bytes_, E, gated, CUS)
+    if KERNELS[k].startswith("narrow"):
+        return KERNELS[k], False
+    tiles = {t: sum(-(-c // t) for c in counts) for t in (64, 128, 256)}
+    name = KERNELS[h.tile(tiles[64], tiles[128], tiles[256], N, -(-K * bytes_ // 128), gated, CUS)]
+    line = (N if kind == "transposed" else K) * bytes_
+    whole = h.whole(N, K * bytes_, E, gated, line)
+    return name, name in TOKENS and bool(h.past(tiles[TOKENS[name]], sum(c > 0 for c in counts), whole))
 
 
 # Segments (rows of each expert), columns and lengths of k that between them reach every kernel
 _SEGMENTS = ([5, 9, 3], [1, 0, 2], [1000, 0, 1], [500, 0, 400, 3], [250] * 4, [1] * 8 + [0] * 8, [10] * 8, [64] * 8,
              [96] * 8, [100, 0, 90, 1], [60] * 16, [11] * 15 + [100], [128] * 16, [45] * 18, [130] * 30,
-             [3000, 0, 4000, 1, 2999], [4] * 64, [300] * 70, [2] * 100)
+             [3000, 0, 4000, 1, 2999], [4] * 64, [300] * 70, [2] * 100, [60] * 44)
 _COLUMNS = (80, 144, 208, 264, 272, 520, 528, 784, 1040, 1408, 2064, 2816, 4096)
-_LENGTHS = (80, 144, 272, 336, 400, 528, 1040, 2064, 4096, 7168)
+_LENGTHS = (80, 144, 272, 336, 400, 528, 1040, 1152, 2064, 4096, 7168)
 
 
 @functools.lru_cache(maxsize=None)
@@ -74,7 +78,7 @@ def case(name, past, bytes_, kind, behind=0):
                 cost = E * N * K * (2 if kind == "gated" else 1) + S * (N + K)
                 if best is not None and cost >= best[0]:
                     continue
-                if product(S, N, K, E, bytes_, kind == "gated", kind == "transposed") == (name, past):
+                if product(counts, N, K, bytes_, kind, behind) == (name, past):
                     best = (cost, (counts, N, K))
     return best[1] if best else None
 

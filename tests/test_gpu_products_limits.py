@@ -66,7 +66,7 @@ def ids(v):
 @pytest.mark.parametrize("counts,N,K", SHAPES, ids=ids)
 def test_bf16(ep, counts, N, K, kind):  # noqa: F811
     E, S = len(counts), sum(counts)
-    say(f"bf16 {kind} E={E} S={S} N={N} K={K} on {choice.product(S, N, K, E, 2, kind == 'gated')}")
+    say(f"bf16 {kind} E={E} S={S} N={N} K={K} on {choice.product(counts, N, K, 2, kind)}")
     g = gen(N + K)
     a = bf16_any(g, S, K)
     w = bf16_any(g, *((E, K, N) if kind == "transposed" else (E, 2 * N if kind == "gated" else N, K)))
@@ -99,7 +99,7 @@ def test_bf16(ep, counts, N, K, kind):  # noqa: F811
 def test_int8(ep, counts, N, K, gated):  # noqa: F811
     K = min(K, MAX - 16)
     E, S = len(counts), sum(counts)
-    say(f"int8 gated={gated} E={E} S={S} N={N} K={K} on {choice.product(S, N, K, E, 1, gated)}")
+    say(f"int8 gated={gated} E={E} S={S} N={N} K={K} on {choice.product(counts, N, K, 1, 'gated' if gated else 'plain')}")
     g = gen(N + K + 1)
     rows = 2 * N if gated else N
     a, w = int8_any(g, S, K), int8_any(g, E, rows, K)
@@ -167,7 +167,7 @@ def long_case(S, N, K, E):
 @pytest.mark.parametrize("S,N,K,E", LONG)
 def test_bf16_long(ep, S, N, K, E, kind):  # noqa: F811
     assert max(S * K, S * N, E * N * K) > 2 ** 31
-    say(f"bf16 {kind} past 2^31: S={S} N={N} K={K} E={E} on {choice.product(S, N, K, E, 2, kind == 'gated')}")
+    say(f"bf16 {kind} past 2^31: S={S} N={N} K={K} E={E}")
     g = gen(S + N)
     if kind == "gated":
         N //= 2
@@ -192,7 +192,7 @@ def test_bf16_long(ep, S, N, K, E, kind):  # noqa: F811
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("S,N,K,E", LONG)
 def test_int8_long(ep, S, N, K, E, gated):  # noqa: F811
-    say(f"int8 past 2^31: S={S} N={N} K={K} E={E} gated={gated} on {choice.product(S, N, K, E, 1, gated)}")
+    say(f"int8 past 2^31: S={S} N={N} K={K} E={E} gated={gated}")
     g = gen(S + N + 1)
     if gated:
         N = max(16, N // 32 * 16)
