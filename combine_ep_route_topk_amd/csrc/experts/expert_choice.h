@@ -82,7 +82,8 @@ inline GemmKernel choose_gemm(int64_t S, int64_t N, int64_t E, bool gated, int64
 
 // ------------------------------------------------------------- bf16 and int8 products
 // Tiles of so many weight rows x tokens: persistent ones of the kernel whose waves
-// split the tile, and narrow ones of the kernel whose waves share k.
+// split the tile, and narrow ones of the kernel whose waves share k; those of 32 x 32 with
+// three stages, or with two and two workgroups a CU.
 enum ProductKernel {
     kProduct256x256,
     kProduct256x128,
@@ -90,8 +91,8 @@ enum ProductKernel {
     kProduct256x64,
     kProduct128x64,
     kNarrow64x64,
-    kNarrow32x64,
     kNarrow32x32,
+    kNarrow32x32Paired,
     kProductKernels,
 };
 constexpr int kProductTiles = kNarrow64x64;      // the persistent ones come first
@@ -100,32 +101,33 @@ constexpr float kLookUs = 1.0f;                  // and look at the segments bef
 // What a tile takes on MI355X, us: `tile`, and `step` for each 128 bytes of k.  Fitted to 4970
 // measured sizes (1 to 64 experts of 1 to 2500 rows on average, even, as even picks
 // fall or by a Zipf law, 64 to 8192 weight rows, 128 to 8192 values of k, bf16 either way
-// round, gated and int8, weights from memory): what is chosen by them takes 0.9% longer than
-// the best on average (1.3% by the Zipf law), 9% at the 97th percentile, twice as long at the worst
-// (a few rows on fewer experts than they could fall on).  With the row tiles estimated
-// from sizes, and not counted in the segments, it was 2.2%, 20% and 2 times.  What the best
-// of the others takes without one of them, on average and at the worst: 256 x 256 1.8% and
-// 59%, 256 x 128 1.3% and 38%, 128 x 128 0.9% and 54%, 256 x 64 0.6% and 27%, 128 x 64
-// 1.8% and 36%, narrow 64 x 64 1.2% and 57%, 32 x 64 0.9% and 40%, 32 x 32 6.3% and 57%.
-// For instance, us (bf16, weights from memory):
-//                                          256x256 256x128 128x128 256x64 128x64 32x32
-//   8 experts x 4096 x 7168, 8 rows each                     75      93     70     77
-//   16 x 2816 x 4096, 64                                     79      61     77    131
+// round, gated and int8, weights from memory): what is chosen by them takes 1.0% longer than
+// the best on average, 10% at the 97th percentile, 1.6 times as long at the worst.  With the
+// row tiles estimated from sizes, and not counted in the segments, it was 2.2%, 20% and 2
+// times.  What the best of the others takes without one of them, on average and at the
+// worst: 256 x 256 1.8% and 59%, 256 x 128 1.3% and 38%, 128 x 128 0.9% and 54%, 256 x 64
+// 0.6% and 27%, 128 x 64 1.7% and 36%, narrow 64 x 64 1.0% and 57%, 32 x 32 2.5% and 62%,
+// paired 2.7% and 43%; 32 x 64 would have spared 0.3% and 36%.
+// For instance, us (bf16, weights from memory; narrow 32 x 32 with three stages / paired):
+//                                          256x256 256x128 128x128 256x64 128x64   32x32
+//   8 experts x 4096 x 7168, 8 rows each                     75      93     70   86 / 82
+//   16 x 2816 x 4096, 64                                     79      61     77
 //   16 x 2816 x 4096, 128                    89      67      99
 //   8 x 4096 x 7168, 500                    173     217     257
 //   1 x 4096 x 4096, 1024                    78      54      39      48
-//   4 x 2048 x 4096, 8                                               44     28     14
-//   1 x 4096 x 7168, 8                                               78     46     16
+//   4 x 2048 x 4096, 40                                              44     28   23 / 19
+//   1 x 4096 x 7168, 8                                               78     46   17 / 23
+//   1 x 512 x 512, 8                                                            3.8 / 3.5
 struct ProductTile {
-    int weights, tokens;
+    int weights, tokens, groups;     // groups: workgroups a CU
     float step, tile;
 };
 EP_BOTH ProductTile product_tile(int kernel)
 {
     constexpr ProductTile tiles[kProductKernels] = {
-        {256, 256, 1.25f, 4.2f}, {256, 128, 0.89f, 1.85f}, {128, 128, 0.53f, 2.0f},
-        {256, 64, 0.795f, 1.1f}, {128, 64, 0.395f, 1.1f},  {64, 64, 0.39f, 2.15f},
-        {32, 64, 0.377f, 1.95f}, {32, 32, 0.363f, 1.95f},
+        {256, 256, 1, 1.11f, 4.6f}, {256, 128, 1, 0.83f, 2.05f}, {128, 128, 1, 0.46f, 2.3f},
+        {256, 64, 1, 0.725f, 1.4f}, {128, 64, 1, 0.40f, 1.0f},   {64, 64, 1, 0.39f, 2.05f},
+        {32, 32, 1, 0.355f, 2.5f},  {32, 32, 2, 0.395f, 1.8f},
     };
     return tiles[kernel];
 }
@@ -133,7 +135,7 @@ EP_BOTH ProductTile product_tile(int kernel)
 EP_BOTH float product_us(int kernel, float tiles, int blocks, int cus)
 {
     const ProductTile t = product_tile(kernel);
-    float rounds = tiles / float(cus);
+    float rounds = tiles / float(cus * t.groups);
     if (kernel < kProductTiles) {
         // each XCD has an eighth of the tiles, and its workgroups take them in turn
         const int share = (int(tiles) + 7) / 8, slots = cus / 8;
@@ -175,12 +177,13 @@ EP_BOTH bool product_past_caches(int row_tiles, int used, bool whole_lines)
 }
 
 // Whether a call takes the persistent kernel, which looks at the segments itself, or a
-// narrow one.  The host knows sizes only: rows spread evenly between 0.4 and 1.6 of the
-// average, and their square root more or less.
+// narrow one.  The host knows sizes only: rows on as many experts as even picks fall on,
+// spread evenly between 0.4 and 1.6 of the average, and their square root more or less.
 // N: columns of the result; row_bytes: of a row of k; gated: 2 N weight rows.
 inline int choose_product(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bool gated, int64_t cus)
 {
-    const double used = double(S < E ? S : E), rows = double(S) / used;
+    const double used = fmax(double(E) * (1.0 - pow(1.0 - 1.0 / double(E), double(S))), 1.0);
+    const double rows = double(S) / used;
     const int blocks = int((row_bytes + 127) / 128);
     auto upto = [](double x) {               // integral of ceil from 0
         return x <= 0.0 ? 0.0 : floor(x) * (floor(x) + 1.0) / 2.0 + ceil(x) * (x - floor(x));

@@ -526,7 +526,7 @@ struct NarrowShape {
     static constexpr int TN = 32 * FN, TM = 32 * FM;
     static constexpr int kColumns = GATED ? TN / 2 : TN;
     static constexpr int kLds = 4 * STAGES * (TN + TM) * 128;
-    static constexpr int kOccupancy = kLds > 80 * 1024 ? 1 : kLds > 160 * 1024 / 3 ? 2 : 3;
+    static constexpr int kOccupancy = kLds > 80 * 1024 ? 1 : 2;
     static constexpr bool kHalves = GATED && FN == 1;     // gate and up share a fragment
     static_assert(!GATED || FN <= 2, "gate rows, then their up rows");
     static_assert(FN <= 2, "a row of a transposed stage is a line at most");

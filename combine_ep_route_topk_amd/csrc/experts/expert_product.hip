@@ -11,8 +11,8 @@ hipError_t launch(const ProductArgs& p, hipStream_t s)
 {
     switch (choose_product(p.S, p.N, int64_t(p.K) * T::kBytes, p.E, KIND >= kGated, device_cu_count())) {
         case kNarrow64x64: return launch_narrow<NarrowShape<T, KIND, 2, 2, 2>>(p, s);
-        case kNarrow32x64: return launch_narrow<NarrowShape<T, KIND, 1, 2, 3>>(p, s);
         case kNarrow32x32: return launch_narrow<NarrowShape<T, KIND, 1, 1, 3>>(p, s);
+        case kNarrow32x32Paired: return launch_narrow<NarrowShape<T, KIND, 1, 1, 2>>(p, s);
         default: return launch_product<T, KIND>(p, s);
     }
 }

@@ -8,7 +8,8 @@ import tempfile
 
 from expert_choice import CUS, HEADER
 
-KERNELS = ["256x256", "256x128", "128x128", "256x64", "128x64", "narrow 64x64", "narrow 32x64", "narrow 32x32"]
+KERNELS = ["256x256", "256x128", "128x128", "256x64", "128x64", "narrow 64x64", "narrow 32x32",
+           "narrow 32x32 paired"]
 # tokens of the tiles that may read the weights past the caches
 TOKENS = {"256x128": 128, "128x128": 128, "256x64": 64, "128x64": 64}
 
