@@ -166,11 +166,25 @@ EP_BOTH int choose_product_tile(int tiles64, int tiles128, int tiles256, int N, 
     return best;
 }
 
+// The last, partly filled round of 256 x 256 tiles, `rest` of them for `slots` CUs: how often
+// their rows are halved, as long as one round of the pieces holds them (256 x 128 and 256 x 64,
+// a workgroup that has a piece through in two thirds of the time).  us whole / in pieces:
+// 8 experts x 4096 x 7168, 500 rows each as picks fall 292 / 248; 2 x 7168 (gated) x 1408, 718
+// rows 69 / 63; 16 x 2816 x 1408, 1433 rows by a Zipf law 190 / 174; int8 8 x 2048 x 4096, 1431
+// rows 102 / 97; no size took longer in pieces.  Counted in the estimates above it
+// would take 256 x 256 where 256 x 128 is faster (8 x 2048 (gated) x 4096, 598 rows 148 / 164).
+EP_BOTH int product_tail(int rest, int slots)
+{
+    return rest * 4 <= slots ? 2 : rest * 2 <= slots ? 1 : 0;
+}
+
 // Whether such a tile reads the weights past the caches: where each of them is read once.
 // Past / through the caches, weights from memory: 0.89 to 0.96 with 64 MB and more, 0.87 to 0.98
 // with less (but 33 MB that the last call left there would take 15 us instead of 11); with
 // more rows than a tile holds 1.0 to 1.2; with rows of k that do not begin on lines 1.0 to
-// 1.15.
+// 1.15.  256 x 256, where this also gives every tile of weights a turn of k: 0.73 to 0.88 at
+// sizes that are powers of two (16 experts x 4096 x 4096, 256 rows 144 / 123 us; 64 x 2048 x
+// 2048, 220 rows 166 / 121), 0.98 on average at any.
 EP_BOTH bool product_past_caches(int row_tiles, int used, bool whole_lines)
 {
     return whole_lines && row_tiles <= used;

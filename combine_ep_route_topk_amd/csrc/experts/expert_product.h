@@ -89,9 +89,10 @@ struct Segments {
     int row_tiles, begin, end;
 };
 
-// The workgroup's share of the tiles of shape P.
+// What the workgroup has of a part of the tiles, in shape P.
 template <class P>
-__device__ __forceinline__ void product_tiles(const ProductArgs& p, const Segments& segments, uint8_t* lds)
+__device__ __forceinline__ void product_tiles(const ProductArgs& p, const Segments& segments,
+                                              const GemmShare& share, uint8_t* lds)
 {
     typedef typename P::T T;
     constexpr int FN = P::FN, FM = P::FM, TN = P::TN, TM = P::TM, STAGES = P::STAGES;
@@ -107,8 +108,8 @@ __device__ __forceinline__ void product_tiles(const ProductArgs& p, const Segmen
     const int wn = wave % P::WN, wm = wave / P::WN;
     const int N = p.N, row_bytes = p.K * T::kBytes;
     const int blocks = (row_bytes + kBK - 1) / kBK;
-    const GemmTiles tiles(TM, (N + P::kColumns - 1) / P::kColumns, segments.row_tiles, segments.begin,
-                          segments.end);
+    const GemmTiles tiles(TM << share.halved, (N + P::kColumns - 1) / P::kColumns, segments.row_tiles,
+                          segments.begin, segments.end);
 
     // LDS image of rows of 128 bytes: chunk c of 16 at slot c ^ (row / 2 % 8), so that
     // the 16 lanes that read one chunk of 16 rows touch every bank once.  A load
@@ -253,7 +254,7 @@ __device__ __forceinline__ void product_tiles(const ProductArgs& p, const Segmen
         }
     };
 
-    GemmTile t = tiles.at(p, TM, 0);
+    GemmTile t = tiles.at(p, TM, 0, share);
     if (t.rows.expert < 0) return;
     // a tile's loads reach into the next one only
     const int steps = blocks > STAGES - 1 ? blocks : STAGES - 1;
@@ -274,7 +275,7 @@ __device__ __forceinline__ void product_tiles(const ProductArgs& p, const Segmen
     int wslot = 0, xslot = 0;                            // the stages of this step
 
     for (int turn = 1;; ++turn) {
-        const GemmTile tnext = tiles.at(p, TM, turn);
+        const GemmTile tnext = tiles.at(p, TM, turn, share);
         if (steps == STAGES - 1) cursor = start(tnext);
         Source w = weights_source(cursor);
 #pragma unroll
@@ -472,28 +473,42 @@ __global__ __launch_bounds__(256, 1) void expert_product_kernel(ProductArgs p, i
         tiles[i] = tiles[i] < limit ? tiles[i] : limit;
     }
     const int blocks = (p.K * T::kBytes + 127) / 128;
-    const int kernel = choose_product_tile(tiles[0], tiles[1], tiles[2], p.N, blocks, KIND >= kGated,
-                                           int(gridDim.x));
+    int kernel = choose_product_tile(tiles[0], tiles[1], tiles[2], p.N, blocks, KIND >= kGated,
+                                     int(gridDim.x));
     const int tokens = product_tile(kernel).tokens;
     found.row_tiles = tokens == 64 ? tiles[0] : tokens == 128 ? tiles[1] : tiles[2];
-    const bool past = product_past_caches(found.row_tiles, used, whole_lines != 0);
+    bool past = product_past_caches(found.row_tiles, used, whole_lines != 0);
+    GemmShare share = kWholeShare;
+    if (kernel == kProduct256x256) {
+        // whole rounds, then the last one in pieces
+        constexpr int kColumns = KIND >= kGated ? 128 : 256;
+        const int all = (found.row_tiles * ((p.N + kColumns - 1) / kColumns) + 7) / 8;
+        const int slots = int(gridDim.x / 8), rest = all % slots;
+        const int halved = rest && all > slots ? product_tail(rest, slots) : 0;
+        if (halved) share.last = all - rest;
+        if (past) product_tiles<ProductShape<T, KIND, 4, 4, 2, 3, true, true>>(p, found, share, lds);
+        else product_tiles<ProductShape<T, KIND, 4, 4, 2, 3, false, false>>(p, found, share, lds);
+        if (!halved) return;
+        kernel = halved == 2 ? kProduct256x64 : kProduct256x128;
+        past = false;                    // the pieces of a tile read the same weights
+        share = {all - rest, all, halved};
+    }
     switch (kernel) {
-        case kProduct256x256: product_tiles<ProductShape<T, KIND, 4, 4, 2, 3, false, false>>(p, found, lds); break;
         case kProduct256x128:
-            if (past) product_tiles<ProductShape<T, KIND, 4, 2, 2, 3, true, true>>(p, found, lds);
-            else product_tiles<ProductShape<T, KIND, 4, 2, 2, 3, true, false>>(p, found, lds);
+            if (past) product_tiles<ProductShape<T, KIND, 4, 2, 2, 3, true, true>>(p, found, share, lds);
+            else product_tiles<ProductShape<T, KIND, 4, 2, 2, 3, true, false>>(p, found, share, lds);
             break;
         case kProduct128x128:
-            if (past) product_tiles<ProductShape<T, KIND, 2, 2, 2, 4, true, true>>(p, found, lds);
-            else product_tiles<ProductShape<T, KIND, 2, 2, 2, 4, true, false>>(p, found, lds);
+            if (past) product_tiles<ProductShape<T, KIND, 2, 2, 2, 4, true, true>>(p, found, kWholeShare, lds);
+            else product_tiles<ProductShape<T, KIND, 2, 2, 2, 4, true, false>>(p, found, kWholeShare, lds);
             break;
         case kProduct256x64:
-            if (past) product_tiles<ProductShape<T, KIND, 2, 2, 4, 3, true, true>>(p, found, lds);
-            else product_tiles<ProductShape<T, KIND, 2, 2, 4, 3, true, false>>(p, found, lds);
+            if (past) product_tiles<ProductShape<T, KIND, 2, 2, 4, 3, true, true>>(p, found, share, lds);
+            else product_tiles<ProductShape<T, KIND, 2, 2, 4, 3, true, false>>(p, found, share, lds);
             break;
         default:
-            if (past) product_tiles<ProductShape<T, KIND, 2, 1, 2, 4, true, true>>(p, found, lds);
-            else product_tiles<ProductShape<T, KIND, 2, 1, 2, 4, true, false>>(p, found, lds);
+            if (past) product_tiles<ProductShape<T, KIND, 2, 1, 2, 4, true, true>>(p, found, kWholeShare, lds);
+            else product_tiles<ProductShape<T, KIND, 2, 1, 2, 4, true, false>>(p, found, kWholeShare, lds);
     }
 }
 

@@ -17,6 +17,12 @@ struct GemmTile {
     RowTile rows;    // rows.expert = -1: none
     int n;           // n tile
 };
+// Part of every XCD's share: its tiles from `first` to before `last`, their rows halved
+// so many times.
+struct GemmShare {
+    int first, last, halved;
+};
+constexpr GemmShare kWholeShare = {0, 1 << 30, 0};
 struct GemmTiles {
     int mt, nt;          // row tiles, n tiles
     int b, end, upto;    // up to 64 experts: lane's segment, and the tiles up to its end
@@ -48,13 +54,26 @@ struct GemmTiles {
     // gridDim / 8.
     template <class Args>
     __device__ __forceinline__ GemmTile at(const Args& p, int TM, int turn) const {
+        return at(p, TM, turn, kWholeShare);
+    }
+    // The same of the pieces, of TM rows, of a part of the share.  A piece behind its tile's
+    // rows has none.
+    template <class Args>
+    __device__ __forceinline__ GemmTile at(const Args& p, int TM, int turn, const GemmShare& of) const {
+        const int slot = int(blockIdx.x / 8) + turn * int(gridDim.x / 8);
+        GemmTile t = find(p, TM << of.halved, of.first + (slot >> of.halved), of.last);
+        const int row = t.rows.row0 + (slot & ((1 << of.halved) - 1)) * TM;
+        t.rows.row0 = row < t.rows.end ? row : t.rows.end;
+        return t;
+    }
+    template <class Args>
+    __device__ __forceinline__ GemmTile find(const Args& p, int TM, int in_share, int last) const {
         GemmTile t;
         t.rows = RowTile{-1, 0, 0};
         t.n = 0;
         const int total = mt * nt, per = (total + 7) / 8;
-        const int in_share = int(blockIdx.x / 8) + turn * int(gridDim.x / 8);
         const int id = int(blockIdx.x % 8) * per + in_share;
-        if (in_share >= per || id >= total) return t;
+        if (in_share >= (last < per ? last : per) || id >= total) return t;
         constexpr int kGroup = 8;
         const int group = id / (kGroup * nt);
         const int gsize = mt - group * kGroup < kGroup ? mt - group * kGroup : kGroup;

@@ -19,6 +19,9 @@ def test_known_sizes():
     # many rows, a tile's rows, few rows, few tiles
     assert choice.product([4096] * 8, 7168, 4096) == ("256x256", False)
     assert choice.product([500] * 8, 4096, 7168) == ("256x256", False)
+    assert choice.product([500] * 7 + [600], 4096, 7168) == ("256x256 last in quarters", False)
+    assert choice.product([500] * 2 + [600] * 6, 4096, 7168) == ("256x256 last in halves", False)
+    assert choice.product([600] * 7 + [800], 4096, 7168) == ("256x256", False)
     assert choice.product([128] * 16, 2816, 4096) == ("256x128", True)
     assert choice.product([64] * 16, 2816, 4096) == ("256x64", True)
     assert choice.product([8] * 8, 4096, 7168) == ("128x64", True)
@@ -43,8 +46,9 @@ def test_past_the_caches():
 
 @pytest.mark.parametrize("E", [1, 3, 64, 1024])
 def test_any_size_has_a_kernel(E):
+    known = choice.KERNELS + list(choice.TAILS.values())
     for rows in (1, 2, 63, 1000, 1 << 19):
         for N in (8, 16, 1000, 1 << 17):
             for K in (8, 16, 1000, 1 << 17):
                 for kind in ("plain", "gated"):
-                    assert choice.product([rows] * E, N, K, kind=kind)[0] in choice.KERNELS
+                    assert choice.product([rows] * E, N, K, kind=kind)[0] in known
