@@ -628,6 +628,8 @@ def _shape(t: torch.Tensor, name: str, dims: int) -> tuple:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.numel() >> 31 and max(t.shape) >> 31:      # the ABI's sizes are 32 bits
+        raise ValueError(f"{name}'s dimensions must be < 2^31, got {tuple(t.shape)}")
     return tuple(t.shape)
 
 
@@ -881,8 +883,10 @@ def ep_quantize_int8(x: torch.Tensor, q: torch.Tensor | None = None,
         raise TypeError("x must be a torch.Tensor")
     if x.dim() < 2:
         raise ValueError(f"x must have 2 dimensions or more, got {x.dim()}")
-    _bits_ok(x, "x")
     dev, rows, H = x.device, x.shape[:-1], x.shape[-1]
+    if rows.numel() >> 31:                          # as _shape
+        raise ValueError(f"x must have fewer than 2^31 rows, got {rows.numel()}")
+    _bits_ok(x, "x")
     if q is None:
         q = _empty(x.shape, torch.int8, dev, stream)
     else:

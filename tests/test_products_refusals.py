@@ -127,3 +127,19 @@ def _gpu_like(tensor):
         def __new__(cls, v):
             return v.as_subclass(cls)
     return Placed(tensor)
+
+
+def test_sizes_past_the_abi(ep):  # noqa: F811
+    """Sizes are 32 bits in C: larger ones are refused before they are cut."""
+    def many(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    few = many(2, 16, 16)
+    for call in (lambda: ep.ep_quantize_int8(many((1 << 32) + 4, 16)),
+                 lambda: ep.ep_quantize_int8(many(1 << 12, 1 << 20, 16)),
+                 lambda: ep.ep_dispatch_int8(many((1 << 32) + 4, 16), many(4, 2, dtype=torch.int32)),
+                 lambda: ep.ep_expert_gemm_bf16(many((1 << 32) + 4, 16), few, many(3, dtype=torch.int32)),
+                 lambda: ep.ep_expert_swiglu_bf16(many((1 << 32) + 4, 16), few, many(3, dtype=torch.int32)),
+                 lambda: ep.ep_expert_gemm_int8(many((1 << 32) + 4, 16, dtype=torch.int8), None, few, None, None)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
