@@ -20,6 +20,26 @@
 // next step's have landed.  The weights of step s + STAGES - 1 are asked for in the
 // first half of step s, into the stage that step s - 1 left; the tokens of it in the
 // last quarter, into the stage that s itself has just left.
+//
+// Many rows (MI355X, 32768 of them, 8 experts, random values): bf16 x 7168 x 4096
+// transposed 1470 to 1560 us, gated x 7168 x 2048 1530, x 2048 x 7168 795, 1.2 to 1.3
+// PFLOP/s, where the library's dense products reach 1.25 to 1.5; int8 gated 797, down 434,
+// 2.2 to 2.4 PFLOP/s (library 2.3 and 2.0).  Power bounds both: matrix instructions alone,
+// from registers, reach 1.6 to 1.7 PFLOP/s on such bf16 values (2.4 on zeros) and 3.3 on
+// int8; in bf16 the matrix unit is busy 77% of the time at 1.6 GHz.  Without its stores
+// 3 to 6% faster, with all loads from L2 6 to 8%.  Accumulators of 32 x 32 rather than
+// 16 x 16 (1.72 against 1.62 from registers) for the same reason: half the operand reads.
+// int8 with a short k (2048: 235 us for 16384 rows x 7168, 52% busy) also pays for its
+// epilogue, 3 us a tile that nothing else on its CU hides: the accumulators take the
+// registers of a second workgroup.
+// Few rows: the weights' bytes.  8 x 4096 x 7168 bf16, 64 rows 74 us, 6.4 TB/s; int8, 256
+// uneven rows 45 us, 5.3 TB/s (launch, segments and the first loads, 5 us, are the same
+// of half as many bytes); one row each 69 and 37, 6.8 and 6.4 TB/s.
+// The steps there, the decode, ragged, training and int8 prefill sizes of the kernel as it
+// was first (us, 64 x 8 x 4096 x 7168 / 1000 rows x 16 x 4096 x 2816 transposed / 32768 x 8 x 7168
+// x 4096 transposed / int8 16384 x 8 x 7168 x 2048): 207 / 192 / 8849 / 513; now 74 / 51 /
+// 1480 / 235.  A stage more (128 x 64, 128 x 128, 256 x 64), or whole steps in registers: within
+// 3%.
 #pragma once
 
 #include "expert_choice.h"
@@ -532,6 +552,10 @@ hipError_t launch_product(const ProductArgs& p, hipStream_t s)
 // share k instead: wave v takes the blocks v, v + 4, .. of 128 bytes, through stages
 // of its own, without a barrier.  Their sums meet in LDS, in the waves' order; wave v
 // finishes the rows 8 v .. 8 v + 7 of each 32.
+// Bound by the latency of a few steps in a row: 1 x 4096 x 7168 of 8 rows (bf16, 59 MB)
+// 17 us, 3.5 TB/s, where the persistent 128 x 64 tile takes 46; 4 x 2048 x 4096 of 40 rows
+// 19 (28), 1 x 512 x 512 of 8 rows 3.5 (5), of which a launch is 2.  Eight waves with two
+// stages each, for four with three: within 3%.
 template <class T_, ProductKind KIND_, int FN_, int FM_, int STAGES_>
 struct NarrowShape {
     typedef T_ T;

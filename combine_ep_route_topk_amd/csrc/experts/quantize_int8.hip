@@ -5,6 +5,12 @@
 // bits, so 127 x / m either is a half integer, which a correctly rounded f32
 // quotient keeps, or is 2^-9 away from one at least.  A row with an infinity or a NaN
 // gets the scale NaN and zeros: its products are NaN.
+//
+// Bytes bound it, 2 H read and (H + 4) written for each copy of a row: a row is read once
+// and kept in registers from its maximum to its values, by one wave up to 2048 values
+// and by four up to 8192.  MI355X, H = 7168: 4096 tokens to 8 rows each 49 us, 6.0 TB/s
+// (by a workgroup a row that reads it twice 88); 32768 rows to one 125 us, 5.6 TB/s,
+// reads and writes mixed, where a copy reaches 5.0.  One division a row.
 #include "experts_internal.h"
 
 namespace ep {
