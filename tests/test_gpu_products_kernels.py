@@ -19,9 +19,9 @@ class Case:
     """Operands of one kernel, and the call on them with all outputs: [(tensor [S][..], columns of it that
     stand for one channel)]."""
 
-    def __init__(self, ep, c, behind=BEHIND, save=False):  # noqa: F811
+    def __init__(self, ep, c, behind=BEHIND, save=False, sizes=None):  # noqa: F811
         self.ep, self.bytes, self.kind, self.save = ep, c[0], c[1], save
-        self.counts, self.N, self.K = choice.case(c[2], c[3], c[0], c[1], behind)
+        self.counts, self.N, self.K = sizes or choice.case(c[2], c[3], c[0], c[1], behind)
         self.E, self.S, self.n = len(self.counts), sum(self.counts) + behind, sum(self.counts)
         g = gen(self.S + self.N)
         self.off = offsets_of(self.counts)
@@ -76,10 +76,7 @@ def name(c):
     return choice.label(c[0]) + ("-saved" if c[1] else "") if isinstance(c[1], bool) else choice.label(c)
 
 
-@pytest.mark.parametrize("c", SAVED, ids=name)
-def test_values(ep, c):  # noqa: F811
-    say(f"values on {name(c)}")
-    k = Case(ep, c[0], save=c[1])
+def check_values(k):
     out = k.run(k.buffers())
     for t, fresh in zip(out, k.buffers()):
         assert torch.equal(t[k.n:], fresh[k.n:]), "rows behind the last segment"
@@ -97,6 +94,29 @@ def test_values(ep, c):  # noqa: F811
             ref.check(out[1][lo:hi], y, ref.rounded(y, err), f"gate_up of expert {e}")
     again = k.run(k.buffers())
     assert all(torch.equal(a, b) for a, b in zip(out, again)), "another call, other bits"
+
+
+@pytest.mark.parametrize("c", SAVED, ids=name)
+def test_values(ep, c):  # noqa: F811
+    say(f"values on {name(c)}")
+    check_values(Case(ep, c[0], save=c[1]))
+
+
+# More experts than a wave has lanes, whose tiles are found by a scan, and a last round in pieces:
+# (bytes, kind, halvings, rows of each expert, columns, K)
+SCANNED = [(2, "plain", 1, 520, 520, 272), (2, "transposed", 1, 520, 520, 272), (2, "gated", 1, 520, 264, 272),
+           (1, "plain", 1, 520, 528, 528), (1, "gated", 1, 520, 272, 528), (2, "plain", 2, 700, 1040, 144),
+           (2, "transposed", 2, 700, 1040, 144), (1, "plain", 2, 700, 1040, 272), (1, "gated", 2, 700, 528, 272)]
+
+
+@pytest.mark.parametrize("c", SCANNED, ids=lambda c: "-".join(map(str, c)))
+def test_last_round_of_many_experts(ep, c):  # noqa: F811
+    bytes_, kind, halved, rows, N, K = c
+    counts = [rows + i % 3 for i in range(70)]
+    counts[11], counts[12], counts[13] = 0, 2 * counts[12], counts[13] - 1
+    assert choice.product(counts, N, K, bytes_, kind, BEHIND)[0] == choice.TAILS[halved]
+    say(f"{c}")
+    check_values(Case(ep, c, sizes=(counts, N, K)))
 
 
 def spoil(k):
