@@ -609,6 +609,7 @@ ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32
  *   a bf16 [S][K]   w13 bf16 [E][2I][K]   h bf16 [S][I] out
  *   gate_up bf16 [S][2I] out, or NULL: g and u rounded, for ep_swiglu_grad.
  * With ep_swiglu_grad and ep_expert_wgrad they are a layer and its gradients.
+ * Outputs overlap neither inputs nor one another, here and in the block below.
  * ------------------------------------------------------------------------- */
 ep_status ep_expert_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* expert_offsets,
                               int32_t S, int32_t N, int32_t K, int32_t E, int32_t transposed,
@@ -628,7 +629,8 @@ ep_status ep_expert_swiglu_bf16(const uint16_t* a, const uint16_t* w13, const in
  * ep_quantize_int8: rows as they are; weights [E][N][K] are S = E N rows of K.
  *   x bf16 [S][H]   q i8 [S][H] out   scale f32 [S] out.
  * ep_dispatch_int8: ep_dispatch with the rows quantised on the way, each row once;
- * pos entries outside [0, T*k) are skipped.  T >= 1.
+ * pos entries outside [0, T*k) are skipped, those inside are distinct (values and
+ * scale of a row that two entries name may be of either token).  T >= 1.
  *   send i8 [T*k][H] out   scale f32 [T*k] out.
  *
  * ep_expert_gemm_int8: y[s][n] = a_scale[s] (w_scale[e][n] sum_k a[s][k] W[e][n][k]),
