@@ -884,8 +884,8 @@ def ep_quantize_int8(x: torch.Tensor, q: torch.Tensor | None = None,
     if x.dim() < 2:
         raise ValueError(f"x must have 2 dimensions or more, got {x.dim()}")
     dev, rows, H = x.device, x.shape[:-1], x.shape[-1]
-    if rows.numel() >> 31:                          # as _shape
-        raise ValueError(f"x must have fewer than 2^31 rows, got {rows.numel()}")
+    if max(rows.numel(), H) >> 31:                  # as _shape
+        raise ValueError(f"x's rows and their length must be < 2^31, got {rows.numel()} of {H}")
     _bits_ok(x, "x")
     if q is None:
         q = _empty(x.shape, torch.int8, dev, stream)
