@@ -135,6 +135,7 @@ EP_BOTH ProductTile product_tile(int kernel)
 EP_BOTH float product_us(int kernel, float tiles, int blocks, int cus)
 {
     const ProductTile t = product_tile(kernel);
+    tiles = tiles < 1e9f ? tiles : 1e9f;         // an integer holds them
     float rounds = tiles / float(cus * t.groups);
     if (kernel < kProductTiles) {
         // each XCD has an eighth of the tiles, and its workgroups take them in turn
@@ -157,7 +158,7 @@ EP_BOTH int choose_product_tile(int tiles64, int tiles128, int tiles256, int N, 
         const ProductTile t = product_tile(k);
         const int columns = gated ? t.weights / 2 : t.weights;
         const int rows = t.tokens == 64 ? tiles64 : t.tokens == 128 ? tiles128 : tiles256;
-        const float us = product_us(k, float(rows * ((N + columns - 1) / columns)), blocks, cus);
+        const float us = product_us(k, float(rows) * float((N + columns - 1) / columns), blocks, cus);
         if (k == 0 || us < least) {
             least = us;
             best = k;
@@ -212,7 +213,7 @@ inline int choose_product(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bo
         double each = used == 1.0 ? ceil(rows / t.tokens) : (upto(high) - upto(low)) / (high - low);
         if (each < 1.0) each = 1.0;
         const double tiles = ceil(fmin(used * each, double(S)) * double((N + columns - 1) / columns));
-        const float us = product_us(k, float(fmin(tiles, 1e9)), blocks, int(cus > 8 ? cus : 8)) +
+        const float us = product_us(k, float(tiles), blocks, int(cus > 8 ? cus : 8)) +
                          (k < kProductTiles ? kLookUs : 0.0f);
         if (k == 0 || us < least) {
             least = us;
@@ -221,6 +222,15 @@ inline int choose_product(int64_t S, int64_t N, int64_t row_bytes, int64_t E, bo
     }
     return best;
 }
+
+// The most tiles that a call can make, of the smallest persistent shape.  Their numbers are kept in
+// 32 bits: sizes that can make 2^30 are refused (their y or h would take 8 TB and more).
+inline int64_t product_most_tiles(int64_t S, int64_t N, int64_t E, bool gated)
+{
+    const int64_t columns = gated ? 64 : 128;
+    return (S / 64 + (E < S ? E : S)) * ((N + columns - 1) / columns);
+}
+constexpr int64_t kProductMostTiles = int64_t(1) << 30;
 
 // Whether the weights' rows begin on lines and are more than the caches keep until the
 // next call.

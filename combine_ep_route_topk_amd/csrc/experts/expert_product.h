@@ -538,9 +538,8 @@ hipError_t launch_product(const ProductArgs& p, hipStream_t s)
     const int64_t row_bytes = int64_t(p.K) * T::kBytes;
     const int64_t line_bytes = KIND == kTransposed ? int64_t(p.N) * T::kBytes : row_bytes;
     const bool whole = product_whole_lines(p.N, row_bytes, p.E, KIND >= kGated, line_bytes);
-    // as many tiles as the smallest shape can make
-    ProductArgs least = p;
-    if (!gemm_tiles(least, 64, KIND >= kGated ? 64 : 128)) return hipErrorInvalidConfiguration;
+    if (product_most_tiles(p.S, p.N, p.E, KIND >= kGated) >= kProductMostTiles)
+        return hipErrorInvalidConfiguration;
     const uint32_t cus = device_cu_count() / 8 * 8;
     EP_LAUNCH((expert_product_kernel<T, KIND>), dim3(cus ? cus : 8), dim3(256), 0, s, p, int(whole));
     return hipGetLastError();
