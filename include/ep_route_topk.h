@@ -634,7 +634,9 @@ ep_status ep_expert_swiglu_bf16(const uint16_t* a, const uint16_t* w13, const in
  *   send i8 [T*k][H] out   scale f32 [T*k] out.
  *
  * ep_expert_gemm_int8: y[s][n] = a_scale[s] (w_scale[e][n] sum_k a[s][k] W[e][n][k]),
- * the sum in 32-bit integers, exact, then f32, rounded once to bf16.
+ * the sum in 32-bit integers, exact, then f32 in this order, rounded once to bf16.
+ * w_scale <= 2^97 (weights up to 127 * 2^97): w_scale times the sum is finite then,
+ * here and below, whatever a_scale makes of it.
  *   a i8 [S][K], a_scale f32 [S]   w i8 [E][N][K], w_scale f32 [E][N], 16-byte aligned
  *   y bf16 [S][N] out.  K < 2^17.
  * ep_expert_swiglu_int8: the gated product as above, h rounded to bf16 and
