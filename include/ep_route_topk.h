@@ -609,6 +609,10 @@ ep_status ep_expert_wgrad(const uint16_t* grad_y, const uint16_t* x, const int32
  *   a bf16 [S][K]   w13 bf16 [E][2I][K]   h bf16 [S][I] out
  *   gate_up bf16 [S][2I] out, or NULL: g and u rounded, for ep_swiglu_grad.
  * With ep_swiglu_grad and ep_expert_wgrad they are a layer and its gradients.
+ * Equal calls give equal bits.  The order of a sum follows from how all rows of
+ * the call fall on the experts (they decide the tiles), so a row's last bits may
+ * differ between calls whose other rows differ; those of the 8-bit products below,
+ * whose sums are exact, do not.
  * Outputs overlap neither inputs nor one another, here and in the block below.
  * ------------------------------------------------------------------------- */
 ep_status ep_expert_gemm_bf16(const uint16_t* a, const uint16_t* w, const int32_t* expert_offsets,
