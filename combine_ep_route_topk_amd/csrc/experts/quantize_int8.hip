@@ -1,9 +1,11 @@
 // quantize_int8.hip -- bf16 rows to int8 with one f32 scale a row.
 //
 // m = max(max|x|, 127 2^-126), scale = m / 127, q = round_to_nearest_even(127 x / m).
-// For bf16 x that quotient is decided exactly: 127 x is exact in f32 and m has 8
-// bits, so 127 x / m either is a half integer, which a correctly rounded f32
-// quotient keeps, or is 2^-9 away from one at least.  A row with an infinity or a NaN
+// For bf16 x that quotient is decided exactly: 127 x is exact in f32, and with X, M <
+// 2^8 the mantissas as integers and 2^d the ratio of their units, 127 x / m = 127 X / (M
+// 2^d) is |254 X - h M 2^d| / (M 2^(d+1)) away from a half integer h / 2: it is one, which a
+// correctly rounded f32 quotient keeps, or 1 / (254 X) of itself away at least, more than
+// 2^-16, where such a quotient is off by 2^-24 of itself.  A row with an infinity or a NaN
 // gets the scale NaN and zeros: its products are NaN.
 //
 // Bytes bound it, 2 H read and (H + 4) written for each copy of a row: a row is read once

@@ -26,8 +26,8 @@ def segments(offsets):
 
 # ----------------------------------------------------------------- rows to integers
 def integers(x):
-    """x [..., H] -> (integers as f64, scales f64).  The quotient in f64 is 2^-52 off at most, and a half
-    integer or 2^-9 away from one (m has 8 bits): its rounding is exact."""
+    """x [..., H] -> (integers as f64, scales f64).  The quotient in f64 is off by 2^-52 of itself at most, and a
+    half integer or 2^-16 of itself away from one (x and m have 8 bits): its rounding is exact."""
     v = x.double()
     ok = torch.isfinite(v).all(-1)
     v = torch.where(ok[..., None], v, torch.zeros_like(v))
