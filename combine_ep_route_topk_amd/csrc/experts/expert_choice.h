@@ -108,23 +108,25 @@ constexpr float kLookUs = 1.0f;                  // and look at the segments bef
 // What a tile takes on MI355X, us: `tile`, and `step` for each 128 bytes of k.  Fitted to 4970
 // measured sizes (1 to 64 experts of 1 to 2500 rows on average, even, as even picks
 // fall or by a Zipf law, 64 to 8192 weight rows, 128 to 8192 values of k, bf16 either way
-// round, gated and int8, weights from memory): what is chosen by them takes 1.0% longer than
-// the best on average, 10% at the 97th percentile, 1.6 times as long at the worst.  With the
-// row tiles estimated from sizes, and not counted in the segments, it was 2.2%, 20% and 2
-// times.  What the best of the others takes without one of them, on average and at the
-// worst: 256 x 256 1.8% and 59%, 256 x 128 1.3% and 38%, 128 x 128 0.9% and 54%, 256 x 64
-// 0.6% and 27%, 128 x 64 1.7% and 36%, narrow 64 x 64 1.0% and 57%, 32 x 32 2.5% and 62%,
-// paired 2.7% and 43%; 32 x 64 would have spared 0.3% and 36%.
+// round, gated and int8, weights from memory), before last rounds in pieces and 256 x 256 tiles
+// past the caches were there.  Of 12751 other such sizes, on the kernels as they are: what is
+// chosen by them takes 1.5% longer than the best on average, 14% at the 97th percentile,
+// 1.7 times as long at the worst; with the row tiles estimated from sizes, and not counted
+// in the segments, 2.2%, 18% and 2.4 times.  What the best of the others takes without one of
+// them, on average and at the worst: 256 x 256 2.0% and 59%, 256 x 128 0.7% and 38%, 128 x 128
+// 0.8% and 48%, 256 x 64 0.5% and 23%, 128 x 64 1.4% and 36%, narrow 64 x 64 1.4% and 64%, 32 x
+// 32 2.7% and 63%, paired 2.2% and 46%.  With 128 and 256 experts, 12 sizes, the best or
+// within 4% of it.
 // For instance, us (bf16, weights from memory; narrow 32 x 32 with three stages / paired):
 //                                          256x256 256x128 128x128 256x64 128x64   32x32
-//   8 experts x 4096 x 7168, 8 rows each                     75      93     70   86 / 82
-//   16 x 2816 x 4096, 64                                     79      61     77
-//   16 x 2816 x 4096, 128                    89      67      99
-//   8 x 4096 x 7168, 500                    173     217     257
-//   1 x 4096 x 4096, 1024                    78      54      39      48
-//   4 x 2048 x 4096, 40                                              44     28   23 / 19
-//   1 x 4096 x 7168, 8                                               78     46   17 / 23
-//   1 x 512 x 512, 8                                                            3.8 / 3.5
+//   8 experts x 4096 x 7168, 8 rows each      122      98      71      93     70   86 / 81
+//   16 x 2816 x 4096, 64                        80      63      85      62     77
+//   16 x 2816 x 4096, 128                       85      68      98     107
+//   8 x 4096 x 7168, 500                       186     219     291
+//   1 x 4096 x 4096, 1024                       76      55      41      47
+//   4 x 2048 x 4096, 40                                 52      33      49     31   23 / 18
+//   1 x 4096 x 7168, 8                                          49      80     45   17 / 23
+//   1 x 512 x 512, 8                                                              3.8 / 3.5
 struct ProductTile {
     int weights, tokens, groups;     // groups: workgroups a CU
     float step, tile;

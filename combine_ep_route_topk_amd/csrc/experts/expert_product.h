@@ -14,7 +14,8 @@
 // holds four neighbouring n of one token.  A step is 128 bytes of k of every row:
 // whole lines from memory.  Its loads go straight into LDS, STAGES of the weights and
 // one less of the tokens, the stream running on across tiles, so that a tile's first
-// loads and the stores of the one before it hide behind matrix work.  A step's four
+// loads and the stores of the one before it hide behind matrix work (with more than 64
+// experts the search for the next segment waits for both: expert_tiles.h).  A step's four
 // quarters work on fragments in registers while the next quarter's are read.
 // Before the last quarter all waves meet: this step's stages have been read, the
 // next step's have landed.  The weights of step s + STAGES - 1 are asked for in the

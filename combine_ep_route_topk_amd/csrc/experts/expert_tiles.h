@@ -13,6 +13,12 @@ namespace {
 // to the XCDs in turn); within a share, groups of 8 row tiles x all n tiles, row
 // tiles fastest: the 32 workgroups that an XCD runs at once read 8 row tiles and
 // 4 weight tiles through its L2.
+// Up to 64 experts each lane keeps one segment.  With more a tile's segment is found by a scan
+// of the offsets, one load after another for every 64 experts, whose waits are also for the
+// stores of the tile before and the loads into LDS of the next: MI355X, bf16, us for 64
+// experts with rows / those and 1 / 64 / 192 / 960 without: 64 x 2048 x 1024, 600 rows 178 / 179
+// / 178 / 180 / 183; 64 rows 49.3 / 50.5 / 50.5 / 50.8 / 53.0; 64 x 4096 x 128 (two steps a
+// tile), 300 rows 62.7 / 66.6 / 67.5 / 67.8 / 71.6.
 struct GemmTile {
     RowTile rows;    // rows.expert = -1: none
     int n;           // n tile
